@@ -19,6 +19,14 @@ Entry points (same names as the C ABI, without the ``ssa_`` prefix):
   fit_logspace log-space least-squares fit of (a, b)
   num_qblocks  number of 128-row query blocks of a batch
   get_error    synchronise and read/clear the device status word
+The training step around the forward (module ``training`` has it as autograd
+functions):
+  fwd_lse      the forward, also writing each row's log-sum-exp; K and V may
+               have fewer heads than Q
+  bwd          its gradients, dense or on the tiles the forward kept
+  save_fp8, restore_fp8   activations in 8 bits, a scale per 128 tokens and head
+  bwd_fp8      bwd on Q, K and V saved in 8 bits
+  rotary       rotary positions on Q and K, or their adjoint
 """
 from __future__ import annotations
 
@@ -75,6 +83,26 @@ def _load():
     L.ssa_calibrate.argtypes = [vp, vp, vp, vp, i32, i32, i32, i32, i32, f32, vp, i32, vp, vp, i32, vp]
     L.ssa_calibrate_ex.restype = i32
     L.ssa_calibrate_ex.argtypes = [vp, vp, vp, vp, i32, i32, i32, i32, i32, f32, vp, i32, vp, vp, i32, vp, vp]
+    i64 = ctypes.c_int64
+    L.ssa_fwd_lse.restype = i32
+    L.ssa_fwd_lse.argtypes = [vp, vp, vp, vp, i32, i32, i32, i32, i32, i32, f32, f32, vp, vp, vp, i32, vp, vp]
+    L.ssa_bwd_workspace_bytes.restype = i64
+    L.ssa_bwd_workspace_bytes.argtypes = [i32, i32, i32]
+    L.ssa_bwd.restype = i32
+    L.ssa_bwd.argtypes = [vp, vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, i32, f32, vp, i32, vp, vp, vp, vp, i64,
+                          vp]
+    L.ssa_save_fp8.restype = i32
+    L.ssa_save_fp8.argtypes = [vp, vp, vp, i32, i32, i32, vp]
+    L.ssa_restore_fp8.restype = i32
+    L.ssa_restore_fp8.argtypes = [vp, vp, vp, i32, i32, i32, vp]
+    L.ssa_bwd_fp8_workspace_bytes.restype = i64
+    L.ssa_bwd_fp8_workspace_bytes.argtypes = [i32, i32, i32, i32, i32]
+    L.ssa_bwd_fp8.restype = i32
+    L.ssa_bwd_fp8.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, i32, f32, vp, i32, vp,
+                              vp, vp, vp, i64, vp]
+    L.ssa_rotary.restype = i32
+    L.ssa_rotary.argtypes = [vp, vp, vp, vp, i64, i64, i64, i64, i32, i32, i32, i32, vp, i32, vp, vp, i32, i32, f32,
+                             i32, vp]
     L.ssa_resolve.restype = f64
     L.ssa_resolve.argtypes = [f64, f64, f64]
     L.ssa_fit_logspace.restype = i32
@@ -325,6 +353,315 @@ def calibrate_fp8(q8, k8, v, cu_seqlens, max_seqlen: int, q_descale: float, k_de
     else:
         _check(_lib.ssa_calibrate_fp8(*head, *tail), "ssa_calibrate_fp8")
     return out, counts
+
+
+def _run(dev, stream, tensors, body):
+    """``body(stream handle)`` with ``dev`` current and on ``stream`` (default:
+    the device's current one), so that what it allocates belongs to the stream
+    its kernels run on. ``tensors`` and the tensors it returns are kept from
+    reuse until both that stream and the caller's are done with them."""
+    import torch
+
+    current = torch.cuda.current_stream(dev)
+    if stream is None:
+        stream = current
+    elif stream.device != dev:
+        raise ValueError(f"stream is on {stream.device}, the tensors on {dev}")
+    if stream == current and torch.cuda.current_device() == dev.index:
+        return body(ctypes.c_void_p(stream.cuda_stream))
+    with torch.cuda.device(dev), torch.cuda.stream(stream):
+        result = body(ctypes.c_void_p(stream.cuda_stream))
+    if stream != current:
+        for t in tensors:
+            if t is not None:
+                t.record_stream(stream)
+        for t in result:
+            if t is not None:
+                t.record_stream(current)
+    return result
+
+
+def _no_overlap(outputs, inputs):
+    """Refuse an output that shares memory with an input or another output
+    (all contiguous): the kernels read and write them in no fixed order."""
+    spans = []
+    for t, name in inputs + outputs:
+        spans.append((t.data_ptr(), t.data_ptr() + t.numel() * t.element_size(), name) if t is not None else None)
+    n = len(inputs)
+    for i, a in enumerate(spans[n:], n):
+        for b in spans[:i]:
+            if a and b and a[0] < b[1] and b[0] < a[1]:
+                raise ValueError(f"{a[2]} overlaps {b[2]}")
+
+
+def _check_shared_heads(q, k, v, cu_seqlens, qkv_dtype):
+    """Checks of fwd_lse and the backward passes: K and V may have fewer heads."""
+    import torch
+
+    if not (isinstance(q, torch.Tensor) and q.is_cuda):
+        raise ValueError("q must be a CUDA tensor")
+    total, H, D = _shape(q)
+    dev = q.device
+    _require(q, "q", qkv_dtype, dev)
+    _require(k, "k", qkv_dtype, dev)
+    if k.dim() != 3 or k.shape[0] != total or k.shape[2] != D or k.shape[1] < 1 or H % k.shape[1] != 0:
+        raise ValueError(f"k has shape {tuple(k.shape)}, expected [{total}, a divisor of {H}, {D}]")
+    _require(v, "v", qkv_dtype, dev, tuple(k.shape))
+    _require(cu_seqlens, "cu_seqlens", torch.int32, dev)
+    if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2:
+        raise ValueError("cu_seqlens must be a 1-D tensor of batch + 1 offsets")
+    return dev, total, H, k.shape[1], D, cu_seqlens.numel() - 1
+
+
+def fwd_lse(q, k, v, cu_seqlens, max_seqlen: int, threshold_scale_factor: float = 0.0, softmax_scale: float = 0.0,
+            out=None, lse=None, skip_counter=None, decision_bitmap=None, stream=None):
+    """The forward of a training step: fwd() plus the rows' log-sum-exp over
+    the kept tiles (natural logarithm of the scaled scores), which bwd() needs.
+    q: CUDA bf16 [total_tokens, H, D]; k, v: [total_tokens, Hkv, D] with Hkv a
+    divisor of H (query head h reads head h // (H // Hkv)). Returns (out,
+    lse[H, total_tokens] float32). With a threshold, pass ``decision_bitmap``
+    (as in fwd) to keep the decisions for bwd()."""
+    import torch
+
+    dev, total, H, Hkv, D, batch = _check_shared_heads(q, k, v, cu_seqlens, torch.bfloat16)
+    _require(out, "out", torch.bfloat16, dev, tuple(q.shape), allow_none=True)
+    _require(lse, "lse", torch.float32, dev, (H, total), allow_none=True)
+    nq = _per_unit_qblocks(dev, H, total, batch, _forward_outputs(skip_counter, decision_bitmap, None, max_seqlen))
+    _no_overlap([(out, "out"), (lse, "lse"), (skip_counter, "skip_counter"), (decision_bitmap, "decision_bitmap")],
+                [(q, "q"), (k, "k"), (v, "v"), (cu_seqlens, "cu_seqlens")])
+
+    def body(handle):
+        o = torch.empty_like(q) if out is None else out
+        r = torch.empty((H, total), dtype=torch.float32, device=dev) if lse is None else lse
+        _check(_lib.ssa_fwd_lse(_ptr(q), _ptr(k), _ptr(v), _ptr(cu_seqlens), batch, total, int(max_seqlen), H, Hkv, D,
+                                float(softmax_scale), float(threshold_scale_factor), _ptr(o), _ptr(r),
+                                _ptr(skip_counter), nq, _ptr(decision_bitmap), handle), "ssa_fwd_lse")
+        return o, r
+
+    return _run(dev, stream, (q, k, v, cu_seqlens, out, lse, skip_counter, decision_bitmap), body)
+
+
+def _backward(what, dout, q, k, v, extra, out, lse, cu_seqlens, max_seqlen, softmax_scale, decision_bitmap, dq, dk, dv,
+              workspace, stream, qkv_dtype, workspace_bytes, call):
+    import torch
+
+    dev, total, H, Hkv, D, batch = _check_shared_heads(q, k, v, cu_seqlens, qkv_dtype)
+    bf16, q_shape, k_shape = torch.bfloat16, (total, H, D), (total, Hkv, D)
+    _require(dout, "dout", bf16, dev, q_shape)
+    _require(out, "out", bf16, dev, q_shape)
+    _require(lse, "lse", torch.float32, dev, (H, total))
+    _require(dq, "dq", bf16, dev, q_shape, allow_none=True)
+    _require(dk, "dk", bf16, dev, k_shape, allow_none=True)
+    _require(dv, "dv", bf16, dev, k_shape, allow_none=True)
+    _require(workspace, "workspace", None, dev, allow_none=True)
+    for t, name, heads in extra:
+        _require(t, name, torch.float32, dev, ((total + TILE - 1) // TILE, heads))
+    nq = _per_unit_qblocks(dev, H, total, batch, [(decision_bitmap, "decision_bitmap", (torch.int32, torch.uint32),
+                                                    (bitmap_words(max_seqlen),))])
+    _no_overlap([(dq, "dq"), (dk, "dk"), (dv, "dv"), (workspace, "workspace")],
+                [(dout, "dout"), (q, "q"), (k, "k"), (v, "v"), (out, "out"), (lse, "lse"), (cu_seqlens, "cu_seqlens"),
+                 (decision_bitmap, "decision_bitmap")] + [(t, name) for t, name, _ in extra])
+    need = workspace_bytes(total, batch, H, Hkv, D)
+    if need < 0:
+        raise SSAError(int(need), what)
+
+    def body(handle):
+        ws = torch.empty(need, dtype=torch.uint8, device=dev) if workspace is None else workspace
+        grads = [torch.empty(shape, dtype=bf16, device=dev) if t is None else t
+                 for t, shape in ((dq, q_shape), (dk, k_shape), (dv, k_shape))]
+        _check(call(_ptr(dout), _ptr(out), _ptr(lse), _ptr(cu_seqlens), batch, total, int(max_seqlen), H, Hkv, D,
+                    float(softmax_scale), _ptr(decision_bitmap), nq, *[_ptr(g) for g in grads], _ptr(ws),
+                    ws.numel() * ws.element_size(), handle), what)
+        return tuple(grads)
+
+    return _run(dev, stream, (dout, q, k, v, out, lse, cu_seqlens, decision_bitmap, dq, dk, dv, workspace)
+                + tuple(t for t, _, _ in extra), body)
+
+
+def bwd(dout, q, k, v, out, lse, cu_seqlens, max_seqlen: int, softmax_scale: float = 0.0, decision_bitmap=None,
+        dq=None, dk=None, dv=None, workspace=None, stream=None):
+    """Gradients of fwd_lse(): returns (dq, dk, dv) in bf16 for the output
+    gradient ``dout``. ``out``, ``lse`` and, when the forward skipped tiles,
+    ``decision_bitmap`` are what it wrote (the decisions count as constants).
+    Rows outside every sequence are left as they were in dq, dk and dv (when
+    they are allocated here, undefined). ``workspace``: a device buffer of at
+    least bwd_workspace_bytes() that no other call uses meanwhile."""
+    import torch
+
+    return _backward(
+        "ssa_bwd", dout, q, k, v, [], out, lse, cu_seqlens, max_seqlen, softmax_scale, decision_bitmap, dq, dk, dv,
+        workspace, stream, torch.bfloat16, lambda total, batch, H, Hkv, D: _lib.ssa_bwd_workspace_bytes(total, batch, H),
+        lambda g, *rest: _lib.ssa_bwd(g, _ptr(q), _ptr(k), _ptr(v), *rest))
+
+
+def bwd_fp8(dout, q_saved, k_saved, v_saved, out, lse, cu_seqlens, max_seqlen: int, softmax_scale: float = 0.0,
+            decision_bitmap=None, dq=None, dk=None, dv=None, workspace=None, stream=None):
+    """bwd() on Q, K and V saved in 8 bits: each ``*_saved`` is save_fp8()'s
+    (codes, scales), and the gradients are those at the restored values."""
+    import torch
+
+    (q, qs), (k, ks), (v, vs) = q_saved, k_saved, v_saved
+    heads = lambda t: t.shape[1] if t.dim() == 3 else -1
+    return _backward(
+        "ssa_bwd_fp8", dout, q, k, v, [(qs, "q_scales", heads(q)), (ks, "k_scales", heads(k)), (vs, "v_scales", heads(v))],
+        out, lse, cu_seqlens, max_seqlen, softmax_scale, decision_bitmap, dq, dk, dv, workspace, stream, torch.uint8,
+        _lib.ssa_bwd_fp8_workspace_bytes,
+        lambda g, *rest: _lib.ssa_bwd_fp8(g, _ptr(q), _ptr(qs), _ptr(k), _ptr(ks), _ptr(v), _ptr(vs), *rest))
+
+
+def bwd_workspace_bytes(total_tokens: int, batch: int, num_heads: int) -> int:
+    """Size of bwd()'s workspace."""
+    n = int(_lib.ssa_bwd_workspace_bytes(int(total_tokens), int(batch), int(num_heads)))
+    if n < 0:
+        raise SSAError(n, "ssa_bwd_workspace_bytes")
+    return n
+
+
+def bwd_fp8_workspace_bytes(total_tokens: int, batch: int, num_heads: int, num_kv_heads: int, head_dim: int) -> int:
+    """Size of bwd_fp8()'s workspace."""
+    n = int(_lib.ssa_bwd_fp8_workspace_bytes(int(total_tokens), int(batch), int(num_heads), int(num_kv_heads),
+                                             int(head_dim)))
+    if n < 0:
+        raise SSAError(n, "ssa_bwd_fp8_workspace_bytes")
+    return n
+
+
+def save_fp8(x, codes=None, scales=None, stream=None):
+    """Save activations in 8 bits: x is CUDA bf16 [total_tokens, H, D] (D 64 or
+    128). Returns (codes uint8 [total_tokens, H, D], scales float32
+    [ceil(total_tokens / 128), H]): E4M3 codes of x / scale, the scale of each
+    128 tokens and head the smallest power of two that keeps them in range."""
+    import torch
+
+    if not (isinstance(x, torch.Tensor) and x.is_cuda):
+        raise ValueError("x must be a CUDA tensor")
+    total, H, D = _shape(x)
+    dev, s_shape = x.device, ((total + TILE - 1) // TILE, H)
+    _require(x, "x", torch.bfloat16, dev)
+    _require(codes, "codes", torch.uint8, dev, tuple(x.shape), allow_none=True)
+    _require(scales, "scales", torch.float32, dev, s_shape, allow_none=True)
+    _no_overlap([(codes, "codes"), (scales, "scales")], [(x, "x")])
+
+    def body(handle):
+        c = torch.empty(x.shape, dtype=torch.uint8, device=dev) if codes is None else codes
+        s = torch.empty(s_shape, dtype=torch.float32, device=dev) if scales is None else scales
+        _check(_lib.ssa_save_fp8(_ptr(x), _ptr(c), _ptr(s), total, H, D, handle), "ssa_save_fp8")
+        return c, s
+
+    return _run(dev, stream, (x, codes, scales), body)
+
+
+def restore_fp8(codes, scales, out=None, stream=None):
+    """What save_fp8() kept: bf16 scale * decode(code), exactly."""
+    import torch
+
+    if not (isinstance(codes, torch.Tensor) and codes.is_cuda):
+        raise ValueError("codes must be a CUDA tensor")
+    total, H, D = _shape(codes)
+    dev = codes.device
+    _require(codes, "codes", torch.uint8, dev)
+    _require(scales, "scales", torch.float32, dev, ((total + TILE - 1) // TILE, H))
+    _require(out, "out", torch.bfloat16, dev, tuple(codes.shape), allow_none=True)
+    _no_overlap([(out, "out")], [(codes, "codes"), (scales, "scales")])
+
+    def body(handle):
+        x = torch.empty(codes.shape, dtype=torch.bfloat16, device=dev) if out is None else out
+        _check(_lib.ssa_restore_fp8(_ptr(codes), _ptr(scales), _ptr(x), total, H, D, handle), "ssa_restore_fp8")
+        return (x,)
+
+    return _run(dev, stream, (codes, scales, out), body)[0]
+
+
+def _rows(t, name, dev, total, dim):
+    """Check a rotary operand [total, H, dim] whose tokens may lie apart (a
+    slice of a fused projection, say); returns its token stride."""
+    import torch
+
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.device != dev or t.dtype != torch.bfloat16:
+        raise ValueError(f"{name} is {t.dtype} on {t.device}, expected torch.bfloat16 on {dev}")
+    if t.dim() != 3 or t.shape[0] != total or t.shape[2] != dim:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected [{total}, heads, {dim}]")
+    H = t.shape[1]
+    if (dim > 1 and t.stride(2) != 1) or (H > 1 and t.stride(1) != dim) or (total > 1 and t.stride(0) < H * dim):
+        raise ValueError(f"{name}: the heads of a token must be contiguous and tokens must not overlap")
+    return t.stride(0) if total > 1 else H * dim
+
+
+def _rows_overlap(a, a_stride, b, b_stride):
+    """Whether two operands of _rows() share an element."""
+    size, n = a.element_size(), a.shape[0]
+    wa, wb = a.shape[1] * a.shape[2] * size, b.shape[1] * b.shape[2] * size
+    pa, pb, sa, sb = a.data_ptr(), b.data_ptr(), a_stride * size, b_stride * size
+    if n == 0 or pa + (n - 1) * sa + wa <= pb or pb + (n - 1) * sb + wb <= pa:
+        return False
+    if sa != sb:
+        return True
+    d = (pb - pa) % sa  # the same stride: b's rows start d bytes into a's
+    return d < wa or d + wb > sa
+
+
+def rotary(q, k, positions, inv_freq, sections=None, interleaved: bool = False, scale: float = 1.0,
+           transpose: bool = False, out_q=None, out_k=None, stream=None):
+    """Rotary positions on Q and, unless it is None, on K, in one launch.
+    q, k: CUDA bf16 [total_tokens, heads, D], each token's heads contiguous;
+    positions: int32 [total_tokens] or [total_tokens, axes]; inv_freq: float64
+    [pairs], radians per position (module ``positions`` makes them). The first
+    2 * pairs elements of a head are rotated, pair i being (2i, 2i + 1) when
+    ``interleaved``, else (i, i + pairs); ``sections`` gives the number of
+    consecutive pairs that turn with each axis. ``transpose`` applies the
+    adjoint: it turns output gradients into input gradients. ``out_q`` may be
+    q itself, ``out_k`` k itself. Returns (q', k')."""
+    import torch
+
+    if not (isinstance(q, torch.Tensor) and q.is_cuda):
+        raise ValueError("q must be a CUDA tensor")
+    total, H, D = _shape(q)
+    dev = q.device
+    _require(positions, "positions", torch.int32, dev)
+    axes = 1 if positions.dim() == 1 else positions.shape[-1]
+    if tuple(positions.shape) not in ((total,), (total, axes)):
+        raise ValueError(f"positions has shape {tuple(positions.shape)}, expected [{total}] or [{total}, axes]")
+    _require(inv_freq, "inv_freq", torch.float64, dev)
+    if inv_freq.dim() != 1 or 2 * inv_freq.numel() > D:
+        raise ValueError(f"inv_freq must be 1-D with at most {D // 2} frequencies")
+    if sections is None and axes > 1:
+        raise ValueError("sections must say how many pairs turn with each of the position axes")
+    counts = [inv_freq.numel()] if sections is None else [int(n) for n in sections]
+    if len(counts) != axes or min(counts) < 0 or sum(counts) != inv_freq.numel():
+        raise ValueError(f"sections must be {axes} counts adding up to {inv_freq.numel()}")
+    Hk = 0 if k is None else k.shape[1]
+    xs = [_rows(q, "q", dev, total, D), 0 if k is None else _rows(k, "k", dev, total, D)]
+    ys = [H * D, Hk * D]
+    written = []
+    for i, (o, name, x) in enumerate(((out_q, "out_q", q), (out_k, "out_k", k))):
+        if o is None:
+            continue
+        if x is None:
+            raise ValueError("out_k without k")
+        ys[i] = _rows(o, name, dev, total, D)
+        if o.shape != x.shape:
+            raise ValueError(f"{name} has shape {tuple(o.shape)}, expected {tuple(x.shape)}")
+        written.append((o, ys[i], name))
+        for y, stride, other in ((q, xs[0], "q"), (k, xs[1], "k")):
+            if y is None or (y is x and o.data_ptr() == x.data_ptr() and ys[i] == stride):
+                continue  # in place: a pair is read and written by one thread
+            if _rows_overlap(o, ys[i], y, stride):
+                raise ValueError(f"{name} overlaps {other}")
+    if len(written) == 2 and _rows_overlap(written[0][0], written[0][1], written[1][0], written[1][1]):
+        raise ValueError("out_q overlaps out_k")
+    n_pairs = (ctypes.c_int32 * axes)(*counts)
+
+    def body(handle):
+        oq = torch.empty((total, H, D), dtype=torch.bfloat16, device=dev) if out_q is None else out_q
+        ok = torch.empty((total, Hk, D), dtype=torch.bfloat16, device=dev) if out_k is None and Hk else out_k
+        _check(_lib.ssa_rotary(_ptr(q), _ptr(k), _ptr(oq), _ptr(ok), xs[0], xs[1], ys[0], ys[1], total, H, Hk, D,
+                               _ptr(positions), axes, n_pairs, _ptr(inv_freq), 2 * inv_freq.numel(),
+                               1 if interleaved else 0, float(scale), 1 if transpose else 0, handle), "ssa_rotary")
+        return oq, ok
+
+    return _run(dev, stream, (q, k, positions, inv_freq, out_q, out_k), body)
 
 
 def resolve(a: float, b: float, target_sparsity: float) -> float:

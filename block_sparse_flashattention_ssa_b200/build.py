@@ -11,8 +11,9 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 SO = os.path.join(PKG, "libssa.so")
-SOURCES = [os.path.join(CSRC, f) for f in ("ssa_kernel.cu", "ssa_host.cpp")]
-DEPS = SOURCES + [os.path.join(CSRC, "sm100.cuh"), os.path.join(INCLUDE, "ssa.h")]
+SOURCES = [os.path.join(CSRC, f) for f in ("ssa_kernel.cu", "ssa_bwd.cu", "ssa_rotary.cu", "ssa_saved.cu",
+                                             "ssa_host.cpp")]
+DEPS = SOURCES + [os.path.join(CSRC, f) for f in ("sm100.cuh", "ssa_internal.h")] + [os.path.join(INCLUDE, "ssa.h")]
 NVCC_FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a", "-lineinfo", "-O3", "-std=c++17",
               "-Xcompiler", "-fPIC", "-shared", "-cudart", "static"]
 

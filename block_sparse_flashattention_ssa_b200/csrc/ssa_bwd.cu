@@ -1,0 +1,737 @@
+// Backward pass of the (skip-softmax) attention forward for B200 (sm_100a).
+//
+// With c the softmax scale, L_r the row log-sum-exp the forward wrote and the
+// sums taken over the KV tiles the forward kept:
+//   P_rj  = exp(c q_r.k_j - L_r)              (recomputed)
+//   D_r   = sum_d dO_rd O_rd
+//   dV_j  = sum_r P_rj dO_r
+//   dS_rj = P_rj (dO_r.v_j - D_r)
+//   dQ_r  = c sum_j dS_rj k_j,  dK_j = c sum_r dS_rj q_r
+// The forward's decisions are constants: no gradient flows through them.
+//
+// A first kernel forms D and -L log2 e per row, padded to whole query blocks
+// (rows past a sequence end get -inf, so their probabilities vanish). The
+// main kernel's CTAs each own 128 output rows and walk the other side's tiles:
+//   kv role: 128 rows of K, V of one K/V head against every query block of the
+//            sequence and every query head of its group that kept the tile;
+//            S^T = K Q^T, dP^T = V dO^T, dV += P^T dO, dK += dS^T Q;
+//   q role:  128 query rows against the KV tiles they kept;
+//            S = Q K^T, dP = dO V^T, dQ += dS K.
+// Both roles are one pipeline with the operands exchanged ("fixed" tiles A, B
+// loaded once; "ring" tiles A, B streamed): S = fixA ringA^T, dP = fixB
+// ringB^T, accA += dS ringA, and in the kv role accB += P ringB. S and dP are
+// formed twice (7 products instead of 5), and in exchange every output row has
+// one owner: no atomics, no fp32 dQ in memory, and results that do not depend
+// on the order in which CTAs run.
+//
+// Warps 0-7: element-wise work, 64 columns of one of the 128 TMEM lanes per
+// thread; warp 8: TMA producer; warp 9: tcgen05 issuer (one thread).
+// TMEM (512 columns): S [0,128), dP [128,256), accA [256,256+D); kv role:
+// accB [384,384+D), P as bf16 pairs over S (columns [0,32) and [64,96)), dS
+// over dP likewise; q role: dS in two buffers [384,448) and [448,512), so S
+// and dP of the next tile are formed as soon as this tile's have been read.
+// MMAs issued by one thread execute in order, so an MMA that overwrites S or
+// dP cannot pass the one ahead of it that reads P or dS in the same columns.
+//
+// Every wait is bounded in time; one that runs out records SSA_ERR_TIMEOUT in
+// the status word, the other roles leave at their next wait, in-flight loads
+// and MMAs are drained and TMEM is released.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <cstdint>
+#include <initializer_list>
+
+#include "sm100.cuh"
+#include "ssa.h"
+#include "ssa_internal.h"
+
+namespace ssa {
+namespace {
+
+using namespace sm100;
+
+constexpr int kT = SSA_TILE;  // rows of every tile
+constexpr int kTmaWarp = 8;
+constexpr int kMmaWarp = 9;
+constexpr int kThreads = 320;
+constexpr int kAStages = 3;  // ring A lives from its S to its dS product, longer than ring B
+constexpr int kBStages = 2;
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kColS = 0, kColDP = 128, kColAccA = 256, kColAccB = 384, kColDS = 384;
+constexpr uint32_t kFull = 0xFFFFFFFFu;
+constexpr float kLog2e = 1.44269504088896340736f;
+
+struct Params {
+  const int32_t* cu_seqlens;
+  const uint32_t* bitmap;  // forward's skip decisions, or NULL: every tile is kept
+  __nv_bfloat16 *dq, *dk, *dv;
+  const __nv_bfloat16 *out, *dout;
+  const float* lse;
+  float* rows;  // [num_heads][units][2][128]: -L log2 e, then D, per query block
+  int* status;
+  int batch, total_tokens, num_heads, num_kv_heads, bitmap_words, max_tiles;
+  int units;     // bound on the query blocks of the batch: ceil(total / 128) + batch
+  int nq_check;  // query blocks the bitmap was sized for, or -1
+  float scale;   // c
+  float c2;      // fp32(c log2 e), the forward's score factor
+};
+
+struct Unit {
+  int seq, block, S, start, gqb0, nq_total;  // block: 128-row block inside the sequence; gqb0: the sequence's first
+};
+
+struct Ctl {
+  uint64_t fix_full;
+  uint64_t a_full[kAStages], a_empty[kAStages];
+  uint64_t b_full[kBStages], b_empty[kBStages];
+  uint64_t s_full, dp_full;           // MMA results ready
+  uint64_t s_done, dp_done, ds_full;  // element-wise warps: see issue order below
+  uint64_t acc_full, drain;
+  uint32_t tmem_base;
+  int abort_flag;
+  int info[kAStages];  // rows of the ring tile inside the sequence (128 but for the last), or -1: no more tiles
+  Unit u;
+};
+
+template <int D>
+struct Layout {
+  static constexpr int kChunks = D / 64;  // 64 bf16 = 128 B per swizzled row
+  static constexpr int kChunkBytes = kT * 128;
+  static constexpr int kTileBytes = kT * D * 2;
+  static constexpr int kRowBytes = 2 * kT * 4;  // -L log2 e and D of one query block
+  static constexpr int kFixA = 0;
+  static constexpr int kFixB = kTileBytes;
+  static constexpr int kRingA = 2 * kTileBytes;
+  static constexpr int kRingB = kRingA + kAStages * kTileBytes;
+  static constexpr int kRows = kRingB + kBStages * kTileBytes;  // kv role only
+  static constexpr int kCtl = kRows + kBStages * kRowBytes;
+  // No slack to align the base: the kernel declares it 1024-byte aligned (128-byte swizzle atoms).
+  static constexpr int kAlloc = kCtl + static_cast<int>(sizeof(Ctl));
+  static_assert(kAlloc <= 232448, "shared memory beyond the 227 KB a CTA may use");
+};
+
+__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile int* abort_flag, int* status) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = globaltimer_ns();
+  for (uint32_t i = 1;; ++i) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if ((i & 31u) == 0) {
+      if (*abort_flag) return false;
+      if (globaltimer_ns() - t0 > kWaitLimitNs) {
+        *abort_flag = 1;
+        atomicOr(status, kStatusTimeout);
+        return false;
+      }
+    }
+  }
+}
+
+__device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t parity, int* status) {
+  const uint64_t t0 = globaltimer_ns();
+  while (!mbar_try_wait(bar, parity)) {
+    if (globaltimer_ns() - t0 > kWaitLimitNs) {
+      atomicOr(status, kStatusTimeout);
+      return;
+    }
+  }
+}
+
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag, int* status) {
+  return __all_sync(kFull, wait_bar(bar, parity, abort_flag, status));
+}
+
+__device__ __forceinline__ void warp_arrive(uint32_t bar, int lane) {
+  tc_fence_before();
+  __syncwarp();
+  if (lane == 0) mbar_arrive(bar);
+}
+
+// Finds the 128-row block number x of the batch (whole warp) and checks
+// cu_seqlens: u.seq < 0 when there is no such block or the input is
+// inconsistent (negative, decreasing or past total_tokens; with a bitmap, a
+// sequence longer than max_seqlen or another number of query blocks than the
+// bitmap was sized for), which is reported in the status word. Up to 32
+// sequences are numbered longest first, so the longest walks start first;
+// longer batches keep their order. Units are indexed in sequence order.
+__device__ void locate(const Params& p, int x, int lane, bool report, Unit& u) {
+  int seq = -1, block = 0, S = 0, start = 0, gqb0 = 0, bad = 0, total = 0, seen = 0;
+  for (int base = 0; base < p.batch; base += 32) {
+    const int b = base + lane;
+    int lo = 0, len = 0, nq = 0;
+    if (b < p.batch) {
+      lo = p.cu_seqlens[b];
+      const int hi = p.cu_seqlens[b + 1];
+      len = hi - lo;
+      if (lo < 0 || len < 0 || hi > p.total_tokens) bad = 1;
+      nq = bad ? 0 : (len + kT - 1) / kT;
+      if (p.bitmap && nq > p.max_tiles) bad = 1;
+    }
+    int off = nq;  // inclusive prefix sum in sequence order
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int t = __shfl_up_sync(kFull, off, o);
+      if (lane >= o) off += t;
+    }
+    const int sum = __shfl_sync(kFull, off, 31);
+    off -= nq;
+    int first = seen + off;  // number of this sequence's first block in the order of work
+    if (p.batch <= 32) {
+      first = 0;
+      for (int o = 0; o < p.batch; ++o) {
+        const int len_o = __shfl_sync(kFull, len, o), nq_o = __shfl_sync(kFull, nq, o);
+        if (len_o > len || (len_o == len && o < b)) first += nq_o;
+      }
+    }
+    const unsigned who = __ballot_sync(kFull, b < p.batch && x >= first && x < first + nq);
+    if (who) {
+      const int src = __ffs(static_cast<int>(who)) - 1;
+      seq = base + src;
+      block = __shfl_sync(kFull, x - first, src);
+      S = __shfl_sync(kFull, len, src);
+      start = __shfl_sync(kFull, lo, src);
+      gqb0 = __shfl_sync(kFull, total + off, src);
+    }
+    total += sum;
+    seen += sum;
+  }
+  bad = __any_sync(kFull, bad) ? 1 : 0;
+  if (p.nq_check >= 0 && total != p.nq_check) bad = 1;
+  if (lane == 0) {
+    if (bad) {
+      if (report) atomicOr(p.status, kStatusDeviceArg);
+      seq = -1;
+    }
+    u = Unit{seq, block, S, start, gqb0, total};
+  }
+}
+
+// D_r = dO_r.O_r and -L_r log2 e of one query block and head; D / 8 lanes per
+// row, 16 bytes of dO and O each. Bound by the read of dO and O.
+template <int D>
+__global__ void __launch_bounds__(256) rows_kernel(const __grid_constant__ Params p) {
+  __shared__ Unit u;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, head = blockIdx.y;
+  if (warp == 0) locate(p, static_cast<int>(blockIdx.x), lane, blockIdx.x == 0 && head == 0, u);
+  __syncthreads();
+  if (u.seq < 0) return;
+  constexpr int kLanes = D / 8, kRowsAtOnce = 256 / kLanes, kSteps = kT / kRowsAtOnce;
+  const int part = threadIdx.x % kLanes, r0 = threadIdx.x / kLanes;
+  const int rows = min(kT, u.S - u.block * kT);
+  float* dst = p.rows + (static_cast<int64_t>(head) * p.units + u.gqb0 + u.block) * (2 * kT);
+  const int64_t base = (static_cast<int64_t>(u.start + u.block * kT) * p.num_heads + head) * D + part * 8;
+  uint4 a[kSteps], b[kSteps];
+#pragma unroll
+  for (int i = 0; i < kSteps; ++i) {
+    const int r = r0 + i * kRowsAtOnce;
+    a[i] = b[i] = make_uint4(0, 0, 0, 0);
+    if (r < rows) {
+      const int64_t at = base + static_cast<int64_t>(r) * p.num_heads * D;
+      a[i] = *reinterpret_cast<const uint4*>(p.dout + at);
+      b[i] = *reinterpret_cast<const uint4*>(p.out + at);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < kSteps; ++i) {
+    const int r = r0 + i * kRowsAtOnce;
+    const uint32_t x[4] = {a[i].x, a[i].y, a[i].z, a[i].w}, y[4] = {b[i].x, b[i].y, b[i].z, b[i].w};
+    float sum = 0.f;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      sum = fmaf(__uint_as_float(x[k] << 16), __uint_as_float(y[k] << 16), sum);
+      sum = fmaf(__uint_as_float(x[k] & 0xFFFF0000u), __uint_as_float(y[k] & 0xFFFF0000u), sum);
+    }
+#pragma unroll
+    for (int o = kLanes / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
+    if (part == 0) {
+      float bias = -INFINITY;  // past the sequence, or a row that saw nothing: no probability
+      if (r < rows) {
+        const float L = p.lse[static_cast<int64_t>(head) * p.total_tokens + u.start + u.block * kT + r];
+        if (L != -INFINITY) bias = -L * kLog2e;
+      }
+      dst[r] = bias;
+      dst[kT + r] = sum;
+    }
+  }
+}
+
+// One 1-D bulk copy global -> shared, counted on `bar` (16-byte aligned).
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(bar)
+      : "memory");
+}
+
+template <int D, bool Q>
+__device__ __forceinline__ void run_role(const CUtensorMap* tmFixA, const CUtensorMap* tmFixB,
+                                         const CUtensorMap* tmRingA, const CUtensorMap* tmRingB, const Params& p,
+                                         uint8_t* smem, int head) {
+  using L = Layout<D>;
+  Ctl& ctl = *reinterpret_cast<Ctl*>(smem + L::kCtl);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const Unit u = ctl.u;
+  const int nt = (u.S + kT - 1) / kT;  // tiles of the sequence
+  const int group = p.num_heads / p.num_kv_heads;
+  volatile int* abort_flag = &ctl.abort_flag;
+  const uint32_t tmem = ctl.tmem_base;
+  auto a_full = [&](int i) { return smem_u32(&ctl.a_full[i]); };
+  auto a_empty = [&](int i) { return smem_u32(&ctl.a_empty[i]); };
+  auto b_full = [&](int i) { return smem_u32(&ctl.b_full[i]); };
+  auto b_empty = [&](int i) { return smem_u32(&ctl.b_empty[i]); };
+  const uint32_t s_full = smem_u32(&ctl.s_full), dp_full = smem_u32(&ctl.dp_full);
+  const uint32_t s_done = smem_u32(&ctl.s_done), dp_done = smem_u32(&ctl.dp_done), ds_full = smem_u32(&ctl.ds_full);
+  const uint32_t fix_full = smem_u32(&ctl.fix_full), acc_full = smem_u32(&ctl.acc_full);
+
+  if (warp == kTmaWarp) {
+    // ------------------------------------------------------------ producer
+    int it = 0, b_issued = 0;  // ring tiles issued
+    bool ok = true;
+    if (lane == 0) {
+      prefetch_tmap(tmRingA);
+      prefetch_tmap(tmRingB);
+      mbar_arrive_expect_tx(fix_full, 2 * L::kTileBytes);
+      for (int ch = 0; ch < L::kChunks; ++ch) {
+        tma_load_3d(smem_u32(smem + L::kFixA + ch * L::kChunkBytes), tmFixA, fix_full, ch * 64, head,
+                    u.start + u.block * kT);
+        tma_load_3d(smem_u32(smem + L::kFixB + ch * L::kChunkBytes), tmFixB, fix_full, ch * 64, head,
+                    u.start + u.block * kT);
+      }
+    }
+    const int ring_heads = Q ? 1 : group;
+    const int chunks = (nt + 31) / 32;
+    // Bits of the tiles base .. base+31 that this CTA's block skips.
+    auto skipped = [&](int step) -> uint32_t {
+      const int g = step / chunks, base = (step % chunks) * 32;
+      if (!p.bitmap || step >= ring_heads * chunks) return 0u;
+      if (Q) {
+        const int64_t unit = static_cast<int64_t>(head) * u.nq_total + u.gqb0 + u.block;
+        return p.bitmap[unit * p.bitmap_words + base / 32];
+      }
+      const int i = base + lane;
+      const int64_t unit = static_cast<int64_t>(head * group + g) * u.nq_total + u.gqb0 + i;
+      const uint32_t w = i < nt ? p.bitmap[unit * p.bitmap_words + u.block / 32] : 0u;
+      return __ballot_sync(kFull, (w >> (u.block & 31)) & 1u);
+    };
+    uint32_t next = skipped(0);
+    for (int step = 0; step < ring_heads * chunks; ++step) {
+      const int base = (step % chunks) * 32;
+      const int ring_head = Q ? head / group : head * group + step / chunks;
+      uint32_t keep = ~next;
+      if (nt - base < 32) keep &= (1u << (nt - base)) - 1u;
+      next = skipped(step + 1);
+      if (lane == 0) {
+        for (; keep && ok; keep &= keep - 1) {
+          const int t = base + __ffs(static_cast<int>(keep)) - 1;
+          const int sa = it % kAStages, sb = it % kBStages;
+          if (it >= kAStages && !(ok = wait_bar(a_empty(sa), ((it / kAStages) - 1) & 1, abort_flag, p.status))) break;
+          ctl.info[sa] = min(kT, u.S - t * kT);
+          mbar_arrive_expect_tx(a_full(sa), L::kTileBytes);
+          for (int ch = 0; ch < L::kChunks; ++ch)
+            tma_load_3d(smem_u32(smem + L::kRingA + sa * L::kTileBytes + ch * L::kChunkBytes), tmRingA, a_full(sa),
+                        ch * 64, ring_head, u.start + t * kT);
+          const int n = it++;
+          if (n >= kBStages && !(ok = wait_bar(b_empty(sb), ((n / kBStages) - 1) & 1, abort_flag, p.status))) break;
+          if (!Q) {
+            // The row values share ring B's barrier, but are read until dS of
+            // their tile: their slot is free with tile n - 2's ring A stage.
+            const int old = n - kBStages;
+            if (old >= 0 && !(ok = wait_bar(a_empty(old % kAStages), (old / kAStages) & 1, abort_flag, p.status))) break;
+          }
+          mbar_arrive_expect_tx(b_full(sb), L::kTileBytes + (Q ? 0 : L::kRowBytes));
+          if (!Q)
+            bulk_load(smem_u32(smem + L::kRows + sb * L::kRowBytes),
+                      p.rows + (static_cast<int64_t>(ring_head) * p.units + u.gqb0 + t) * (2 * kT), L::kRowBytes,
+                      b_full(sb));
+          for (int ch = 0; ch < L::kChunks; ++ch)
+            tma_load_3d(smem_u32(smem + L::kRingB + sb * L::kTileBytes + ch * L::kChunkBytes), tmRingB, b_full(sb),
+                        ch * 64, ring_head, u.start + t * kT);
+          ++b_issued;
+        }
+      }
+      ok = __shfl_sync(kFull, ok ? 1 : 0, 0) != 0;
+      if (!ok) break;
+    }
+    if (lane == 0) {
+      if (ok) {  // say that there are no more tiles
+        const int sa = it % kAStages;
+        if (it < kAStages || (ok = wait_bar(a_empty(sa), ((it / kAStages) - 1) & 1, abort_flag, p.status))) {
+          ctl.info[sa] = -1;
+          mbar_arrive(a_full(sa));
+        }
+      }
+      if (!ok) {  // drain the loads still in flight before shared memory goes away
+        drain_wait(fix_full, 0, p.status);
+        for (int i = 0; i < kAStages; ++i)
+          if (it > i) drain_wait(a_full(i), ((it - 1 - i) / kAStages) & 1, p.status);
+        for (int i = 0; i < kBStages; ++i)
+          if (b_issued > i) drain_wait(b_full(i), ((b_issued - 1 - i) / kBStages) & 1, p.status);
+      }
+    }
+  } else if (warp == kMmaWarp) {
+    // ------------------------------------------------------- tcgen05 issuer
+    if (lane == 0) {
+      constexpr uint32_t idesc_s = idesc_bf16_f32(kT, kT, false);
+      constexpr uint32_t idesc_acc = idesc_bf16_f32(kT, D, true);
+      // dst = fix ring^T, both K-major with 128-byte swizzle: 32 B of d per MMA.
+      auto product = [&](uint32_t dst, int fix, int ring) {
+        const uint64_t da = smem_desc_sw128(smem_u32(smem + fix), 16, 1024);
+        const uint64_t db = smem_desc_sw128(smem_u32(smem + ring), 16, 1024);
+        const uint32_t a_lo = static_cast<uint32_t>(da), b_lo = static_cast<uint32_t>(db);
+        const uint64_t a_hi = da & 0xFFFFFFFF00000000ull, b_hi = db & 0xFFFFFFFF00000000ull;
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks) {
+          const uint32_t off = ((ks >> 2) * L::kChunkBytes + (ks & 3) * 32) >> 4;
+          mma_ss(tmem + dst, a_hi | (a_lo + off), b_hi | (b_lo + off), idesc_s, ks > 0 ? 1u : 0u);
+        }
+      };
+      // acc += E ring with E (bf16 pairs, 128 x 128) in TMEM and the ring tile
+      // MN-major (d contiguous), 16 of its rows per MMA; `gap` columns lie
+      // between the two halves of E.
+      auto accumulate = [&](uint32_t acc, uint32_t e, uint32_t gap, int ring, bool more) {
+        const uint64_t db = smem_desc_sw128(smem_u32(smem + ring), L::kChunkBytes, 1024);
+        const uint32_t b_lo = static_cast<uint32_t>(db);
+        const uint64_t b_hi = db & 0xFFFFFFFF00000000ull;
+#pragma unroll
+        for (int ks = 0; ks < kT / 16; ++ks)
+          mma_ts(tmem + acc, tmem + e + ks * 8 + (ks >= 4 ? gap : 0), b_hi | (b_lo + (ks * 16 * 128 >> 4)), idesc_acc,
+                 (more || ks > 0) ? 1u : 0u);
+      };
+      auto wait = [&](uint32_t bar, int parity) { return wait_bar(bar, parity, abort_flag, p.status); };
+      auto ring_a = [&](int j) { return L::kRingA + (j % kAStages) * L::kTileBytes; };
+      auto ring_b = [&](int j) { return L::kRingB + (j % kBStages) * L::kTileBytes; };
+      // True when tile j exists; its A tile has landed then.
+      auto has = [&](int j, bool& ok) {
+        ok = wait(a_full(j % kAStages), (j / kAStages) & 1);
+        return ok && *static_cast<volatile int*>(&ctl.info[j % kAStages]) >= 0;
+      };
+      bool ok = wait(fix_full, 0);
+      bool more = ok && has(0, ok);
+      if (more) {
+        tc_fence_after();
+        product(kColS, L::kFixA, ring_a(0));
+        tc_commit(s_full);
+        if ((ok = wait(b_full(0), 0))) {
+          tc_fence_after();
+          product(kColDP, L::kFixB, ring_b(0));
+          tc_commit(dp_full);
+          if (Q) tc_commit(b_empty(0));
+        }
+      }
+      for (int j = 0; ok && more; ++j) {
+        more = has(j + 1, ok);
+        if (!ok) break;
+        if (Q) {
+          // S(j+1) once S(j) is in registers, dP(j+1) once dP(j) is, then dQ += dS(j) K_j.
+          if (more) {
+            if (!(ok = wait(s_done, j & 1))) break;
+            tc_fence_after();
+            product(kColS, L::kFixA, ring_a(j + 1));
+            tc_commit(s_full);
+            if (!(ok = wait(b_full((j + 1) % kBStages), ((j + 1) / kBStages) & 1))) break;
+            if (!(ok = wait(dp_done, j & 1))) break;
+            tc_fence_after();
+            product(kColDP, L::kFixB, ring_b(j + 1));
+            tc_commit(dp_full);
+            tc_commit(b_empty((j + 1) % kBStages));
+          }
+          if (!(ok = wait(ds_full, j & 1))) break;
+          tc_fence_after();
+          accumulate(kColAccA, kColDS + (j & 1) * 64, 0, ring_a(j), j > 0);
+          tc_commit(a_empty(j % kAStages));
+        } else {
+          // dV += P(j)^T dO_j and, behind it, S(j+1) into the same columns;
+          // dK += dS(j)^T Q_j and, behind it, dP(j+1): the element-wise warps
+          // work on dS(j) under the first pair and on P(j+1) under the second.
+          if (!(ok = wait(s_done, j & 1))) break;
+          tc_fence_after();
+          accumulate(kColAccB, kColS, 32, ring_b(j), j > 0);
+          tc_commit(b_empty(j % kBStages));
+          if (more) {
+            product(kColS, L::kFixA, ring_a(j + 1));
+            tc_commit(s_full);
+            if (!(ok = wait(b_full((j + 1) % kBStages), ((j + 1) / kBStages) & 1))) break;
+          }
+          if (!(ok = wait(ds_full, j & 1))) break;
+          tc_fence_after();
+          accumulate(kColAccA, kColDP, 32, ring_a(j), j > 0);
+          tc_commit(a_empty(j % kAStages));
+          if (more) {
+            product(kColDP, L::kFixB, ring_b(j + 1));
+            tc_commit(dp_full);
+          }
+        }
+      }
+      if (ok) {
+        tc_commit(acc_full);
+      } else {
+        tc_commit(smem_u32(&ctl.drain));
+        drain_wait(smem_u32(&ctl.drain), 0, p.status);
+      }
+    }
+  } else {
+    // -------------------------------------------------------- element-wise
+    const int half = warp >> 2;  // columns [64 half, 64 half + 64)
+    const int row = (warp & 3) * 32 + lane;
+    const uint32_t lanes = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+    const bool row_valid = u.block * kT + row < u.S;
+    float row_bias = 0.f, row_delta = 0.f;  // q role: this thread's row
+    if (Q) {
+      const float* r = p.rows + (static_cast<int64_t>(head) * p.units + u.gqb0 + u.block) * (2 * kT);
+      row_bias = r[row];
+      row_delta = r[kT + row];
+    }
+    const float2 c2 = make_float2(p.c2, p.c2);
+    bool ok = true;
+    int j = 0;
+    for (;; ++j) {
+      const int sa = j % kAStages;
+      if (!(ok = warp_wait(a_full(sa), (j / kAStages) & 1, abort_flag, p.status))) break;
+      const int valid = *static_cast<volatile int*>(&ctl.info[sa]);
+      if (valid < 0) break;
+      const float* rows = reinterpret_cast<const float*>(smem + L::kRows + (j % kBStages) * L::kRowBytes) + half * 64;
+      if (!Q && !(ok = warp_wait(b_full(j % kBStages), (j / kBStages) & 1, abort_flag, p.status))) break;
+      if (!(ok = warp_wait(s_full, j & 1, abort_flag, p.status))) break;
+      tc_fence_after();
+      uint32_t s[64];
+      tmem_ld_x64_async(lanes + kColS + half * 64, s);
+      if (valid < kT) {
+        // The tile ends past the sequence. Its rows out there are summation
+        // rows of the accumulating products: they must be zeros, not whatever
+        // memory holds (NaN times a zero probability is NaN).
+        const int words = (kT - valid) * 8;  // 16-byte words of a chunk's rows past the end
+        for (int i = threadIdx.x; i < L::kChunks * words; i += 256) {
+          const int at = (i / words) * L::kChunkBytes + valid * 128 + (i % words) * 16;
+          *reinterpret_cast<uint4*>(smem + L::kRingA + sa * L::kTileBytes + at) = make_uint4(0, 0, 0, 0);
+          if (!Q)
+            *reinterpret_cast<uint4*>(smem + L::kRingB + (j % kBStages) * L::kTileBytes + at) = make_uint4(0, 0, 0, 0);
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      }
+      tmem_wait_ld_tied(s);
+      if (Q) warp_arrive(s_done, lane);
+      // P = 2^(c2 S - L log2 e)
+#pragma unroll
+      for (int i = 0; i < 32; ++i) {
+        const float2 bias = Q ? make_float2(row_bias, row_bias) : reinterpret_cast<const float2*>(rows)[i];
+        const float2 e = ffma2(make_float2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), c2, bias);
+        s[2 * i] = __float_as_uint(ex2_approx(e.x));
+        s[2 * i + 1] = __float_as_uint(ex2_approx(e.y));
+      }
+      if (valid < kT) {  // also where the score of a row past the end was not finite
+#pragma unroll
+        for (int i = 0; i < 64; ++i)
+          if (half * 64 + i >= valid) s[i] = 0u;
+      }
+      uint32_t pk[32];
+      if (!Q) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) pk[i] = pack_bf16x2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1]));
+        tmem_st_x32(lanes + kColS + half * 64, pk);
+        warp_arrive(s_done, lane);
+      }
+      if (!(ok = warp_wait(dp_full, j & 1, abort_flag, p.status))) break;
+      tc_fence_after();
+      uint32_t d[64];
+      tmem_ld_x64_async(lanes + kColDP + half * 64, d);
+      tmem_wait_ld_tied(d);
+      if (Q) warp_arrive(dp_done, lane);
+#pragma unroll
+      for (int i = 0; i < 32; ++i) {
+        const float2 delta = Q ? make_float2(row_delta, row_delta) : reinterpret_cast<const float2*>(rows + kT)[i];
+        float x = __uint_as_float(s[2 * i]) * (__uint_as_float(d[2 * i]) - delta.x);
+        float y = __uint_as_float(s[2 * i + 1]) * (__uint_as_float(d[2 * i + 1]) - delta.y);
+        if (valid < kT) {
+          if (half * 64 + 2 * i >= valid) x = 0.f;
+          if (half * 64 + 2 * i + 1 >= valid) y = 0.f;
+        }
+        pk[i] = pack_bf16x2(x, y);
+      }
+      tmem_st_x32(lanes + (Q ? kColDS + (j & 1) * 64 + half * 32 : kColDP + half * 64), pk);
+      warp_arrive(ds_full, lane);
+    }
+
+    // Epilogue: this thread's row and half of the D columns of each accumulator.
+    const bool any = j > 0;  // no tile was kept: the gradients are zero
+    if (ok) ok = warp_wait(acc_full, 0, abort_flag, p.status);
+    if (ok) {
+      tc_fence_after();
+      const int heads = Q ? p.num_heads : p.num_kv_heads;
+      const int64_t at = (static_cast<int64_t>(u.start + u.block * kT + row) * heads + head) * D + half * (D / 2);
+#pragma unroll
+      for (int a = 0; a < (Q ? 1 : 2); ++a) {
+        __nv_bfloat16* dst = (Q ? p.dq : (a ? p.dv : p.dk)) + at;
+        const float f = a ? 1.f : p.scale;
+#pragma unroll
+        for (int ch = 0; ch < D / 64; ++ch) {
+          uint32_t o[32];
+          tmem_ld_x32(lanes + (a ? kColAccB : kColAccA) + half * (D / 2) + ch * 32, o);
+          if (row_valid) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              uint32_t w[4];
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                w[k] = any ? pack_bf16x2(__uint_as_float(o[8 * i + 2 * k]) * f, __uint_as_float(o[8 * i + 2 * k + 1]) * f)
+                           : 0u;
+              reinterpret_cast<uint4*>(dst + ch * 32)[i] = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+          }
+        }
+      }
+    }
+  }
+}
+
+// blockIdx.x: 128-row block of the batch; blockIdx.y: the K/V heads (kv role,
+// the longer one, first), then the query heads (q role).
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    bwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+               const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmdO,
+               const __grid_constant__ Params p) {
+  using L = Layout<D>;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  Ctl& ctl = *reinterpret_cast<Ctl*>(smem + L::kCtl);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int y = static_cast<int>(blockIdx.y);
+  if (warp == 0) locate(p, static_cast<int>(blockIdx.x), lane, blockIdx.x == 0 && y == 0, ctl.u);
+  __syncthreads();
+  if (ctl.u.seq < 0) return;  // uniform
+
+  if (threadIdx.x == 0) {
+    mbar_init(smem_u32(&ctl.fix_full), 1);
+    for (int i = 0; i < kAStages; ++i) {
+      mbar_init(smem_u32(&ctl.a_full[i]), 1);
+      mbar_init(smem_u32(&ctl.a_empty[i]), 1);
+    }
+    for (int i = 0; i < kBStages; ++i) {
+      mbar_init(smem_u32(&ctl.b_full[i]), 1);
+      mbar_init(smem_u32(&ctl.b_empty[i]), 1);
+    }
+    mbar_init(smem_u32(&ctl.s_full), 1);
+    mbar_init(smem_u32(&ctl.dp_full), 1);
+    mbar_init(smem_u32(&ctl.s_done), 8);
+    mbar_init(smem_u32(&ctl.dp_done), 8);
+    mbar_init(smem_u32(&ctl.ds_full), 8);
+    mbar_init(smem_u32(&ctl.acc_full), 1);
+    mbar_init(smem_u32(&ctl.drain), 1);
+    ctl.abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == kMmaWarp) {
+    tmem_alloc(smem_u32(&ctl.tmem_base), kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+
+  if (y < p.num_kv_heads)
+    run_role<D, false>(&tmK, &tmV, &tmQ, &tmdO, p, smem, y);
+  else
+    run_role<D, true>(&tmQ, &tmdO, &tmK, &tmV, p, smem, y - p.num_kv_heads);
+
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    tc_fence_after();
+    tmem_dealloc(ctl.tmem_base, kTmemCols);
+  }
+}
+
+// ----------------------------------------------------------------- host side
+
+int64_t bound_units(int total_tokens, int batch) { return (static_cast<int64_t>(total_tokens) + kT - 1) / kT + batch; }
+
+template <int D>
+int launch(const Params& p, const void* q, const void* k, const void* v, cudaStream_t stream) {
+  CUtensorMap tq, tk, tv, tdo;
+  if (!internal::bf16_tensor_map(&tq, q, p.total_tokens, p.num_heads, D) ||
+      !internal::bf16_tensor_map(&tk, k, p.total_tokens, p.num_kv_heads, D) ||
+      !internal::bf16_tensor_map(&tv, v, p.total_tokens, p.num_kv_heads, D) ||
+      !internal::bf16_tensor_map(&tdo, p.dout, p.total_tokens, p.num_heads, D))
+    return internal::fail("cuTensorMapEncodeTiled failed or the driver entry point is unavailable");
+  constexpr int smem = Layout<D>::kAlloc;
+  cudaError_t e = cudaFuncSetAttribute(bwd_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return internal::fail(e);
+  const unsigned units = static_cast<unsigned>(p.units);
+  rows_kernel<D><<<dim3(units, static_cast<unsigned>(p.num_heads)), 256, 0, stream>>>(p);
+  if ((e = cudaGetLastError()) != cudaSuccess) return internal::fail(e);
+  bwd_kernel<D><<<dim3(units, static_cast<unsigned>(p.num_heads + p.num_kv_heads)), kThreads, smem, stream>>>(
+      tq, tk, tv, tdo, p);
+  e = cudaGetLastError();
+  return e == cudaSuccess ? SSA_OK : internal::fail(e);
+}
+
+}  // namespace
+}  // namespace ssa
+
+using namespace ssa;
+
+extern "C" int64_t ssa_bwd_workspace_bytes(int total_tokens, int batch, int num_heads) {
+  if (total_tokens < 0 || batch < 1 || num_heads < 1) return SSA_ERR_INVALID_ARG;
+  return bound_units(total_tokens, batch) * num_heads * (2 * kT * static_cast<int64_t>(sizeof(float)));
+}
+
+int internal::check_backward(const Backward& a) {
+  if (!a.cu_seqlens || a.batch < 1 || a.total_tokens < 0 || a.max_seqlen < 0 || a.num_kv_heads < 1 ||
+      a.num_heads < 1 || a.num_heads % a.num_kv_heads != 0 || a.num_heads > 65535 - a.num_kv_heads)
+    return SSA_ERR_INVALID_ARG;
+  if (std::isnan(a.softmax_scale) || std::isinf(a.softmax_scale)) return SSA_ERR_INVALID_ARG;
+  if (a.head_dim != 64 && a.head_dim != 128) return SSA_ERR_UNSUPPORTED;
+  if (a.decision_bitmap && (a.num_qblocks < 0 || a.max_seqlen < 1)) return SSA_ERR_INVALID_ARG;
+  if (a.total_tokens == 0) return SSA_OK;
+  if (bound_units(a.total_tokens, a.batch) > 0x7FFFFFFF) return SSA_ERR_INVALID_ARG;
+  if (a.workspace_bytes < ssa_bwd_workspace_bytes(a.total_tokens, a.batch, a.num_heads)) return SSA_ERR_INVALID_ARG;
+  for (const void* ptr : {a.dout, a.q, a.k, a.v, a.out, static_cast<const void*>(a.dq), static_cast<const void*>(a.dk),
+                          static_cast<const void*>(a.dv), static_cast<const void*>(a.workspace)}) {
+    if (!ptr) return SSA_ERR_INVALID_ARG;
+    if (reinterpret_cast<uintptr_t>(ptr) & 15u) return SSA_ERR_UNSUPPORTED;
+  }
+  if (!a.lse) return SSA_ERR_INVALID_ARG;
+  return device_pointers({a.dout, a.q, a.k, a.v, a.out, a.lse, a.cu_seqlens, a.decision_bitmap, a.dq, a.dk, a.dv,
+                          a.workspace});
+}
+
+int internal::launch_backward(const Backward& a, cudaStream_t stream) {
+  Params p{};
+  if (const int rc = status_word(&p.status); rc != SSA_OK) return rc;
+  p.cu_seqlens = a.cu_seqlens;
+  p.bitmap = a.decision_bitmap;
+  p.dq = static_cast<__nv_bfloat16*>(a.dq);
+  p.dk = static_cast<__nv_bfloat16*>(a.dk);
+  p.dv = static_cast<__nv_bfloat16*>(a.dv);
+  p.out = static_cast<const __nv_bfloat16*>(a.out);
+  p.dout = static_cast<const __nv_bfloat16*>(a.dout);
+  p.lse = a.lse;
+  p.rows = static_cast<float*>(a.workspace);
+  p.batch = a.batch;
+  p.total_tokens = a.total_tokens;
+  p.num_heads = a.num_heads;
+  p.num_kv_heads = a.num_kv_heads;
+  p.max_tiles = static_cast<int>((static_cast<int64_t>(a.max_seqlen) + kT - 1) / kT);
+  p.bitmap_words = (p.max_tiles + 31) / 32;
+  p.units = static_cast<int>(bound_units(a.total_tokens, a.batch));
+  p.nq_check = a.decision_bitmap ? a.num_qblocks : -1;
+  const double c =
+      a.softmax_scale > 0.f ? static_cast<double>(a.softmax_scale) : 1.0 / std::sqrt(static_cast<double>(a.head_dim));
+  p.scale = static_cast<float>(c);
+  p.c2 = static_cast<float>(c * 1.4426950408889634073599246810019);
+  return a.head_dim == 64 ? launch<64>(p, a.q, a.k, a.v, stream) : launch<128>(p, a.q, a.k, a.v, stream);
+}
+
+extern "C" int ssa_bwd(const void* dout, const void* q, const void* k, const void* v, const void* out,
+                       const float* lse, const int32_t* cu_seqlens, int batch, int total_tokens, int max_seqlen,
+                       int num_heads, int num_kv_heads, int head_dim, float softmax_scale,
+                       const uint32_t* decision_bitmap, int num_qblocks, void* dq, void* dk, void* dv,
+                       void* workspace, int64_t workspace_bytes, void* stream) {
+  const internal::Backward a{dout, q, k, v, out, lse, cu_seqlens, batch, total_tokens, max_seqlen, num_heads,
+                             num_kv_heads, head_dim, softmax_scale, decision_bitmap, num_qblocks, dq, dk, dv,
+                             workspace, workspace_bytes};
+  if (const int rc = internal::check_backward(a); rc != SSA_OK || total_tokens == 0) return rc;
+  return internal::launch_backward(a, static_cast<cudaStream_t>(stream));
+}

@@ -56,6 +56,7 @@
 
 #include "sm100.cuh"
 #include "ssa.h"
+#include "ssa_internal.h"
 
 namespace ssa {
 namespace {
@@ -76,9 +77,6 @@ constexpr uint32_t kTmemCols = 512;
 __host__ __device__ constexpr uint32_t col_S(int x) { return x ? 128u : 0u; }    // S_X (and P_X)
 __host__ __device__ constexpr uint32_t col_O(int x) { return x ? 384u : 256u; }  // O_X
 constexpr float kRescaleThreshold = 8.0f;  // log2 units: P stays <= 256 before a rescale
-constexpr uint64_t kWaitLimitNs = 2000000000ull;
-constexpr int kStatusTimeout = 1;
-constexpr int kStatusDeviceArg = 2;
 constexpr uint32_t kFull = 0xFFFFFFFFu;
 constexpr int kVoteBarrier = 1;  // named barriers 1 and 2: the vote of softmax group A and B
 
@@ -106,6 +104,8 @@ struct Params {
   float tsf;  // threshold_scale_factor (kSkip)
   int n_cal;
   float Lcal[SSA_MAX_THRESHOLDS];  // fp32(log2 lambda_k) (kCalib)
+  float* lse;    // LSE: natural-log row sums [num_heads][total_tokens]
+  int kv_group;  // LSE: query heads per K/V head
 };
 
 struct Ctl {
@@ -114,6 +114,7 @@ struct Ctl {
   uint64_t v_full[kVStages], v_empty[kVStages];
   uint64_t s_full[kQBlocks], p_hi[kQBlocks], p_ready[kQBlocks];
   uint64_t o_final, drain;
+  uint64_t v_tail;  // LSE: the last V tile's rows past the sequence end are zero
   uint32_t tmem_base;
   int abort_flag;
   int dec[kQBlocks][kDecRing];  // decision of tile j in slot j % kDecRing: ((j + 1) << 1) | skip
@@ -326,7 +327,12 @@ __device__ void locate_unit(const Params& p, bool need_max, int lane, Ctl& ctl) 
   }
 }
 
-template <int D, int MODE, bool EX, int PREC>
+// LSE (the forward of a training step): also writes each row's log-sum-exp
+// over the kept tiles, lets kv_group query heads share a K/V head, and zeroes
+// the rows of the last V tile that lie past the sequence end, so that whatever
+// stands there (NaN or infinities included) meets its zero probabilities as
+// zeros.
+template <int D, int MODE, bool EX, int PREC, bool LSE>
 __global__ void __launch_bounds__(kThreads, 1)
     ssa_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                          const __grid_constant__ CUtensorMap tmV, const __grid_constant__ Params p) {
@@ -339,6 +345,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   const int head = blockIdx.y;
+  const int head_kv = LSE ? head / p.kv_group : head;
 
   if (warp == 0) locate_unit(p, EX, lane, ctl);
   __syncthreads();
@@ -376,6 +383,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     mbar_init(o_final, 1);
     mbar_init(smem_u32(&ctl.drain), 1);
+    if (LSE) mbar_init(smem_u32(&ctl.v_tail), 1);
     ctl.abort_flag = 0;
     for (int x = 0; x < kQBlocks; ++x)
       for (int i = 0; i < kDecRing; ++i) ctl.dec[x][i] = 0;  // tag 0: no tile yet
@@ -392,6 +400,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp == kTmaWarp) {
     // ------------------------------------------------------------ producer
+    int tail_stage = -1, tail_parity = 0;  // LSE: where the last V tile went, when it ends past the sequence
     if (lane == 0) {
       prefetch_tmap(&tmQ);
       prefetch_tmap(&tmK);
@@ -415,7 +424,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t dst = smem_u32(smem + L::kK + st * L::kQKTileBytes);
           mbar_arrive_expect_tx(k_full(st), L::kQKTileBytes);
           for (int ch = 0; ch < L::kQKChunks; ++ch)
-            tma_load_3d(dst + ch * L::kChunkBytes, &tmK, k_full(st), ch * L::kQKChunkElems, head,
+            tma_load_3d(dst + ch * L::kChunkBytes, &tmK, k_full(st), ch * L::kQKChunkElems, head_kv,
                         seq_start + k_issued * kBN);
         }
         if (!ok) break;
@@ -441,8 +450,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t dst = smem_u32(smem + L::kV + vs * L::kVTileBytes);
           mbar_arrive_expect_tx(v_full(vs), L::kVTileBytes);
           for (int ch = 0; ch < L::kVChunks; ++ch)
-            tma_load_3d(dst + ch * L::kChunkBytes, &tmV, v_full(vs), ch * L::kVChunkElems, head,
+            tma_load_3d(dst + ch * L::kChunkBytes, &tmV, v_full(vs), ch * L::kVChunkElems, head_kv,
                         seq_start + j * kBN);
+          if (LSE && j == nkv - 1 && S % kBN != 0) {
+            tail_stage = vs;
+            tail_parity = (v_issued / kVStages) & 1;
+          }
           ++v_issued;
         }
       }
@@ -452,6 +465,23 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (k_issued > st) drain_wait(k_full(st), ((k_issued - 1 - st) / kKStages) & 1);
         for (int st = 0; st < kVStages; ++st)
           if (v_issued > st) drain_wait(v_full(st), ((v_issued - 1 - st) / kVStages) & 1);
+        tail_stage = -1;
+      }
+    }
+    if (LSE) {
+      __syncwarp();
+      tail_stage = __shfl_sync(kFull, tail_stage, 0);
+      tail_parity = __shfl_sync(kFull, tail_parity, 0);
+      if (tail_stage >= 0 && warp_wait(v_full(tail_stage), tail_parity, abort_flag)) {
+        // whole 128-byte rows: the swizzle moves data inside a row only
+        uint8_t* v_s = smem + L::kV + tail_stage * L::kVTileBytes;
+        const int first = S % kBN, words = (kBN - first) * 8;  // 16-byte words per chunk
+        for (int i = lane; i < L::kVChunks * words; i += 32)
+          *reinterpret_cast<uint4*>(v_s + (i / words) * L::kChunkBytes + first * 128 + (i % words) * 16) =
+              make_uint4(0, 0, 0, 0);
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // seen by the MMA's reads
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&ctl.v_tail));
       }
     }
   } else if (warp == kMmaWarp) {
@@ -544,6 +574,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         bool v_waited = false;
         if (MODE != kSkip) {
           if (!(ok = wait_bar(v_full(v_used % kVStages), (v_used / kVStages) & 1, abort_flag))) break;
+          if (LSE && j == nkv - 1 && S % kBN != 0 &&
+              !(ok = wait_bar(smem_u32(&ctl.v_tail), 0, abort_flag)))
+            break;
           v_waited = true;
         }
         for (int x = 0; x < nx; ++x) {
@@ -559,6 +592,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!(ok = wait_bar(p_hi(x), kept[x] & 1, abort_flag))) break;
             if (!v_waited) {
               if (!(ok = wait_bar(v_full(v_used % kVStages), (v_used / kVStages) & 1, abort_flag))) break;
+              if (LSE && j == nkv - 1 && S % kBN != 0 &&
+                  !(ok = wait_bar(smem_u32(&ctl.v_tail), 0, abort_flag)))
+                break;
               v_waited = true;
             }
             tc_fence_after();
@@ -815,6 +851,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (ok) {
       tc_fence_after();
       const float inv_l = F8V ? p.v_scale / l : 1.0f / l;
+      if (LSE && row_valid)  // m_used is in log2 units: ln sum_c exp(s) = m ln 2 + ln l
+        p.lse[static_cast<int64_t>(head) * p.total_tokens + seq_start + qb * kBM + row] =
+            fmaf(m_used, 0.693147180559945309f, logf(l));
       __nv_bfloat16* orow =
           p.out + (static_cast<int64_t>(seq_start + qb * kBM + row) * p.num_heads + head) * static_cast<int64_t>(D);
 #pragma unroll
@@ -916,6 +955,8 @@ struct Call {
   bool f8v = false;             // V is E4M3 bytes too (and P is rounded to E4M3)
   double qk_descale = 1.0;      // q_descale * k_descale (E4M3 only)
   float v_descale = 1.0f;       // multiplies the output when V is E4M3
+  int Hkv = 0;                  // K/V heads when they differ from H (LSE only)
+  float* lse = nullptr;         // row log-sum-exp output (LSE only)
 };
 
 // True when `p` is device (or managed) memory of the current device: a host
@@ -974,16 +1015,17 @@ Params base_params(const Call& a) {
   return p;
 }
 
-template <int D, int MODE, bool EX, int PREC>
+template <int D, int MODE, bool EX, int PREC, bool LSE = false>
 int launch(const Call& a, const Params& p) {
   CUtensorMap tq, tk, tv;
+  const int Hkv = LSE ? a.Hkv : a.H;
   if (!make_tensor_map(&tq, a.q, a.total_tokens, a.H, D, PREC >= kQK8) ||
-      !make_tensor_map(&tk, a.k, a.total_tokens, a.H, D, PREC >= kQK8) ||
-      !make_tensor_map(&tv, a.v, a.total_tokens, a.H, D, PREC == kQKV8)) {
+      !make_tensor_map(&tk, a.k, a.total_tokens, Hkv, D, PREC >= kQK8) ||
+      !make_tensor_map(&tv, a.v, a.total_tokens, Hkv, D, PREC == kQKV8)) {
     t_last_cuda_error = "cuTensorMapEncodeTiled failed or the driver entry point is unavailable";
     return SSA_ERR_CUDA;
   }
-  auto kernel = ssa_attention_kernel<D, MODE, EX, PREC>;
+  auto kernel = ssa_attention_kernel<D, MODE, EX, PREC, LSE>;
   constexpr int smem = Layout<D, PREC>::kAlloc;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return cuda_fail(e);
@@ -1053,7 +1095,37 @@ int fwd_impl(const Call& a, float tsf, int32_t* skip_counter, int num_qblocks, u
   return ex ? dispatch_d<kDense, true>(a, p) : dispatch_d<kDense, false>(a, p);
 }
 
+template <int MODE, bool EX>
+int dispatch_lse(const Call& a, const Params& p) {
+  return a.D == 64 ? launch<64, MODE, EX, kBf16, true>(a, p) : launch<128, MODE, EX, kBf16, true>(a, p);
+}
+
 }  // namespace
+
+namespace internal {
+
+int fail(cudaError_t e) { return cuda_fail(e); }
+
+int fail(const char* text) {
+  t_last_cuda_error = text;
+  return SSA_ERR_CUDA;
+}
+
+int device_pointers(std::initializer_list<const void*> ptrs) { return check_device_pointers(ptrs); }
+
+bool bf16_tensor_map(CUtensorMap* map, const void* base, int total_tokens, int H, int D) {
+  return make_tensor_map(map, base, total_tokens, H, D, false);
+}
+
+int status_word(int** ptr) {
+  void* at = nullptr;
+  const cudaError_t e = cudaGetSymbolAddress(&at, g_status);
+  if (e != cudaSuccess) return cuda_fail(e);
+  *ptr = static_cast<int*>(at);
+  return SSA_OK;
+}
+
+}  // namespace internal
 }  // namespace ssa
 
 using namespace ssa;
@@ -1119,6 +1191,35 @@ extern "C" int ssa_fwd_ex(const void* q, const void* k, const void* v, const int
   const Call a{q, k, v, cu_seqlens, batch, total_tokens, max_seqlen, num_heads, head_dim, softmax_scale, out,
                static_cast<cudaStream_t>(stream)};
   return fwd_impl(a, threshold_scale_factor, skip_counter, num_qblocks, decision_bitmap, tile_stat);
+}
+
+extern "C" int ssa_fwd_lse(const void* q, const void* k, const void* v, const int32_t* cu_seqlens, int batch,
+                           int total_tokens, int max_seqlen, int num_heads, int num_kv_heads, int head_dim,
+                           float softmax_scale, float threshold_scale_factor, void* out, float* lse,
+                           int32_t* skip_counter, int num_qblocks, uint32_t* decision_bitmap, void* stream) {
+  Call a{q, k, v, cu_seqlens, batch, total_tokens, max_seqlen, num_heads, head_dim, softmax_scale, out,
+         static_cast<cudaStream_t>(stream)};
+  const float tsf = threshold_scale_factor;
+  int rc = validate(a);
+  if (rc != SSA_OK) return rc;
+  if (num_kv_heads < 1 || num_heads % num_kv_heads != 0) return SSA_ERR_INVALID_ARG;
+  if (std::isnan(tsf) || std::isinf(tsf)) return SSA_ERR_INVALID_ARG;
+  if (decision_bitmap && max_seqlen < 1) return SSA_ERR_INVALID_ARG;
+  const bool per_unit = skip_counter || decision_bitmap;
+  if (per_unit && num_qblocks < 0) return SSA_ERR_INVALID_ARG;
+  if (total_tokens == 0) return SSA_OK;
+  if (!lse) return SSA_ERR_INVALID_ARG;
+  if ((rc = check_device_pointers({lse, skip_counter, decision_bitmap})) != SSA_OK) return rc;
+  Params p = base_params(a);
+  p.nq_check = per_unit ? num_qblocks : -1;
+  p.skip_counter = skip_counter;
+  p.bitmap = decision_bitmap;
+  p.tsf = tsf;
+  p.lse = lse;
+  p.kv_group = num_heads / num_kv_heads;
+  a.Hkv = num_kv_heads;
+  if (tsf > 0.f) return decision_bitmap ? dispatch_lse<kSkip, true>(a, p) : dispatch_lse<kSkip, false>(a, p);
+  return decision_bitmap ? dispatch_lse<kDense, true>(a, p) : dispatch_lse<kDense, false>(a, p);
 }
 
 namespace ssa {

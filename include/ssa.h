@@ -223,6 +223,112 @@ int ssa_calibrate_fp8(const void* q, const void* k, const void* v, const int32_t
                       int32_t* counts, int num_qblocks, void* stream);
 
 /*
+ * The training step around the forward. Three operators: the forward that
+ * also writes each row's log-sum-exp (ssa_fwd_lse), the backward pass that
+ * recomputes the probabilities from it (ssa_bwd), on inputs kept in bf16 or
+ * saved in 8 bits (ssa_save_fp8, ssa_bwd_fp8), and rotary positions on Q and K
+ * with their adjoint (ssa_rotary).
+ *
+ * Layout. As above, but K and V may have fewer heads than Q: num_kv_heads
+ * divides num_heads, and query head h reads K/V head
+ * h / (num_heads / num_kv_heads).
+ *
+ * ssa_fwd_lse: ssa_fwd on bf16 inputs, plus
+ *   lse   device float [num_heads][total_tokens]: ln sum_c exp(s_rc) over the
+ *         columns of the kept tiles, s the scaled scores; written for the
+ *         rows of every sequence, other rows are not touched
+ *   decision_bitmap, skip_counter, num_qblocks   as in ssa_fwd_ex, each
+ *         buffer nullable
+ * Memory past a sequence's end may hold anything, NaN included, without effect
+ * on its rows.
+ */
+int ssa_fwd_lse(const void* q, const void* k, const void* v, const int32_t* cu_seqlens, int batch, int total_tokens,
+                int max_seqlen, int num_heads, int num_kv_heads, int head_dim, float softmax_scale,
+                float threshold_scale_factor, void* out, float* lse, int32_t* skip_counter, int num_qblocks,
+                uint32_t* decision_bitmap, void* stream);
+
+/*
+ * Gradients of the forward. With c the softmax scale, P_rj = exp(c q_r.k_j -
+ * lse_r) over the kept tiles and D_r = dout_r.out_r:
+ *   dV_j = sum_r P_rj dout_r,   dS_rj = P_rj (dout_r.v_j - D_r),
+ *   dQ_r = c sum_j dS_rj k_j,   dK_j = c sum_r dS_rj q_r,
+ * the sums of dK and dV over every query head that shares the K/V head. The
+ * skip decisions are taken as constants. P and dS are rounded to bf16 for the
+ * products, which accumulate in fp32; the gradients are rounded to bf16 once.
+ * Results do not depend on the order of execution.
+ *   dout, out         device bf16 [total_tokens, num_heads, head_dim]
+ *   lse               as ssa_fwd_lse wrote it (a row with -inf takes no part)
+ *   decision_bitmap   as ssa_fwd_lse wrote it for the same max_seqlen, or NULL
+ *                     when every tile was kept; num_qblocks is its Q
+ *   dq                device bf16 [total_tokens, num_heads, head_dim]
+ *   dk, dv            device bf16 [total_tokens, num_kv_heads, head_dim]; the
+ *                     rows of every sequence are written (zeros for a block
+ *                     that no tile was kept for), nothing else is touched.
+ *                     They must not overlap the inputs or each other.
+ *   workspace         device memory, 16-byte aligned, of at least
+ *                     ssa_bwd_workspace_bytes() bytes (negative status for
+ *                     sizes out of range); contents need not be kept, but no
+ *                     other call may use it meanwhile
+ */
+int64_t ssa_bwd_workspace_bytes(int total_tokens, int batch, int num_heads);
+int ssa_bwd(const void* dout, const void* q, const void* k, const void* v, const void* out, const float* lse,
+            const int32_t* cu_seqlens, int batch, int total_tokens, int max_seqlen, int num_heads, int num_kv_heads,
+            int head_dim, float softmax_scale, const uint32_t* decision_bitmap, int num_qblocks, void* dq, void* dk,
+            void* dv, void* workspace, int64_t workspace_bytes, void* stream);
+
+/*
+ * Activations saved in 8 bits: E4M3 codes and one scale per 128 consecutive
+ * tokens and head, the smallest power of two s with max |x| <= 448 s (1 where
+ * all are zero, at least 2^-100), code = E4M3(x / s) to nearest even. A value
+ * that is not finite gets the NaN code and does not count for the scale.
+ * ssa_restore_fp8 returns s * decode(code), exact in bf16.
+ *   x       device bf16 [total_tokens, num_heads, head_dim], 16-byte aligned;
+ *           head_dim 64 or 128
+ *   codes   device bytes of the same shape, 8-byte aligned
+ *   scales  device float [ceil(total_tokens / 128)][num_heads]
+ */
+int ssa_save_fp8(const void* x, void* codes, float* scales, int total_tokens, int num_heads, int head_dim,
+                 void* stream);
+int ssa_restore_fp8(const void* codes, const float* scales, void* x, int total_tokens, int num_heads, int head_dim,
+                    void* stream);
+
+/*
+ * ssa_bwd on Q, K and V saved by ssa_save_fp8: the gradients at the restored
+ * values, with the lse and out of the forward (which ran on the values before
+ * they were saved). The workspace also holds the restored tensors.
+ */
+int64_t ssa_bwd_fp8_workspace_bytes(int total_tokens, int batch, int num_heads, int num_kv_heads, int head_dim);
+int ssa_bwd_fp8(const void* dout, const void* q, const float* q_scales, const void* k, const float* k_scales,
+                const void* v, const float* v_scales, const void* out, const float* lse, const int32_t* cu_seqlens,
+                int batch, int total_tokens, int max_seqlen, int num_heads, int num_kv_heads, int head_dim,
+                float softmax_scale, const uint32_t* decision_bitmap, int num_qblocks, void* dq, void* dk, void* dv,
+                void* workspace, int64_t workspace_bytes, void* stream);
+
+/*
+ * Rotary positions on Q and, when num_kv_heads > 0, on K in the same launch.
+ * The first rotary_dim elements of each head form rotary_dim / 2 pairs: pair i
+ * is (2i, 2i+1) when interleaved, else (i, i + rotary_dim / 2). With the angle
+ * t = positions[token][axis of i] * inv_freq[i],
+ *   (a, b) -> scale * (a cos t - b sin t, a sin t + b cos t),
+ * and by -t with transpose != 0: the adjoint, which turns the gradients of the
+ * outputs into those of the inputs. The other elements are copied. Angles are
+ * formed in double; results are rounded to bf16 once.
+ *   q, q_out    device bf16, head h of token t at t * stride + h * head_dim
+ *               (strides in elements, at least num_heads * head_dim); q_out
+ *               may be q itself with the same stride, else they must not overlap
+ *   k, k_out    likewise with num_kv_heads (ignored when that is 0)
+ *   head_dim    a multiple of 8, up to 256; rotary_dim even, <= head_dim
+ *   positions   device int32 [total_tokens][num_axes], num_axes 1 to 4
+ *   sections    HOST int32 [num_axes]: consecutive pairs of each axis, adding
+ *               up to rotary_dim / 2
+ *   inv_freq    device double [rotary_dim / 2], radians per position
+ */
+int ssa_rotary(const void* q, const void* k, void* q_out, void* k_out, int64_t q_stride, int64_t k_stride,
+               int64_t q_out_stride, int64_t k_out_stride, int total_tokens, int num_heads, int num_kv_heads,
+               int head_dim, const int32_t* positions, int num_axes, const int32_t* sections, const double* inv_freq,
+               int rotary_dim, int interleaved, float scale, int transpose, void* stream);
+
+/*
  * threshold_scale_factor = a * exp(b * target_sparsity) (README, "Calibrated
  * threshold"; TRT-LLM VisualGen docs, "Checkpoint Config"). Returns NaN when
  * a <= 0, target_sparsity is outside [0, 1] or an argument is not finite.

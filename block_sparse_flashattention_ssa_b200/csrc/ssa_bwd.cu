@@ -26,12 +26,19 @@
 //
 // Warps 0-7: element-wise work, 64 columns of one of the 128 TMEM lanes per
 // thread; warp 8: TMA producer; warp 9: tcgen05 issuer (one thread).
-// TMEM (512 columns): S [0,128), dP [128,256), accA [256,256+D); kv role:
-// accB [384,384+D), P as bf16 pairs over S (columns [0,32) and [64,96)), dS
-// over dP likewise; q role: dS in two buffers [384,448) and [448,512), so S
-// and dP of the next tile are formed as soon as this tile's have been read.
-// MMAs issued by one thread execute in order, so an MMA that overwrites S or
-// dP cannot pass the one ahead of it that reads P or dS in the same columns.
+// TMEM (512 columns): two score regions X [0,128) and Y [128,256), accA
+// [256,256+D), and
+//   kv role: accB [384,384+D). Tile j has S in one score region and dP in the
+//            other; P and dS, as bf16 pairs, replace S once it is in registers
+//            (P in the first 32 of each 64 columns, dS in the second). S of the
+//            next tile takes the place of dP as soon as that has been read,
+//            and dP of the next tile that of P and dS, behind the products
+//            that read them: the regions change places with every tile.
+//   q role:  S in X, dP in Y, dS in two buffers [384,448) and [448,512), so S
+//            and dP of the next tile are formed as soon as this tile's have
+//            been read.
+// MMAs issued by one thread execute in order, so an MMA that overwrites P or
+// dS cannot pass the one ahead of it that reads them.
 //
 // Every wait is bounded in time; one that runs out records SSA_ERR_TIMEOUT in
 // the status word, the other roles leave at their next wait, in-flight loads
@@ -70,7 +77,7 @@ struct Params {
   __nv_bfloat16 *dq, *dk, *dv;
   const __nv_bfloat16 *out, *dout;
   const float* lse;
-  float* rows;  // [num_heads][units][2][128]: -L log2 e, then D, per query block
+  float* rows;  // [num_heads][units][2][128]: -L log2 e, then -D, per query block
   int* status;
   int batch, total_tokens, num_heads, num_kv_heads, bitmap_words, max_tiles;
   int units;     // bound on the query blocks of the batch: ceil(total / 128) + batch
@@ -88,7 +95,13 @@ struct Ctl {
   uint64_t a_full[kAStages], a_empty[kAStages];
   uint64_t b_full[kBStages], b_empty[kBStages];
   uint64_t s_full, dp_full;           // MMA results ready
-  uint64_t s_done, dp_done, ds_full;  // element-wise warps: see issue order below
+  // Element-wise warps. q role: S is in registers, dP is in registers; kv role
+  // (s_done): P is stored and dP in registers.
+  uint64_t s_done, dp_done;
+  // dS of even and odd tiles is stored. Two, because in the q role S and dP of tile j + 1
+  // are issued before the issuer waits for dS(j): the element-wise warps may
+  // finish both before it looks, and one barrier would have gone round.
+  uint64_t ds_full[2];
   uint64_t acc_full, drain;
   uint32_t tmem_base;
   int abort_flag;
@@ -101,7 +114,7 @@ struct Layout {
   static constexpr int kChunks = D / 64;  // 64 bf16 = 128 B per swizzled row
   static constexpr int kChunkBytes = kT * 128;
   static constexpr int kTileBytes = kT * D * 2;
-  static constexpr int kRowBytes = 2 * kT * 4;  // -L log2 e and D of one query block
+  static constexpr int kRowBytes = 2 * kT * 4;  // -L log2 e and -D of one query block
   static constexpr int kFixA = 0;
   static constexpr int kFixB = kTileBytes;
   static constexpr int kRingA = 2 * kTileBytes;
@@ -208,7 +221,7 @@ __device__ void locate(const Params& p, int x, int lane, bool report, Unit& u) {
   }
 }
 
-// D_r = dO_r.O_r and -L_r log2 e of one query block and head; D / 8 lanes per
+// -D_r = -dO_r.O_r and -L_r log2 e of one query block and head; D / 8 lanes per
 // row, 16 bytes of dO and O each. Bound by the read of dO and O.
 template <int D>
 __global__ void __launch_bounds__(256) rows_kernel(const __grid_constant__ Params p) {
@@ -252,7 +265,7 @@ __global__ void __launch_bounds__(256) rows_kernel(const __grid_constant__ Param
         if (L != -INFINITY) bias = -L * kLog2e;
       }
       dst[r] = bias;
-      dst[kT + r] = sum;
+      dst[kT + r] = -sum;
     }
   }
 }
@@ -282,7 +295,8 @@ __device__ __forceinline__ void run_role(const CUtensorMap* tmFixA, const CUtens
   auto b_full = [&](int i) { return smem_u32(&ctl.b_full[i]); };
   auto b_empty = [&](int i) { return smem_u32(&ctl.b_empty[i]); };
   const uint32_t s_full = smem_u32(&ctl.s_full), dp_full = smem_u32(&ctl.dp_full);
-  const uint32_t s_done = smem_u32(&ctl.s_done), dp_done = smem_u32(&ctl.dp_done), ds_full = smem_u32(&ctl.ds_full);
+  const uint32_t s_done = smem_u32(&ctl.s_done), dp_done = smem_u32(&ctl.dp_done);
+  auto ds_full = [&](int j) { return smem_u32(&ctl.ds_full[j & 1]); };  // phase j >> 1
   const uint32_t fix_full = smem_u32(&ctl.fix_full), acc_full = smem_u32(&ctl.acc_full);
 
   if (warp == kTmaWarp) {
@@ -437,29 +451,30 @@ __device__ __forceinline__ void run_role(const CUtensorMap* tmFixA, const CUtens
             tc_commit(dp_full);
             tc_commit(b_empty((j + 1) % kBStages));
           }
-          if (!(ok = wait(ds_full, j & 1))) break;
+          if (!(ok = wait(ds_full(j), (j >> 1) & 1))) break;
           tc_fence_after();
           accumulate(kColAccA, kColDS + (j & 1) * 64, 0, ring_a(j), j > 0);
           tc_commit(a_empty(j % kAStages));
         } else {
-          // dV += P(j)^T dO_j and, behind it, S(j+1) into the same columns;
-          // dK += dS(j)^T Q_j and, behind it, dP(j+1): the element-wise warps
-          // work on dS(j) under the first pair and on P(j+1) under the second.
+          // Once P(j) is stored and dP(j) in registers: S(j+1) over dP(j), for the
+          // element-wise warps to go on with, and dV += P(j)^T dO_j; once dS(j)
+          // is stored: dK += dS(j)^T Q_j and, over P(j) and dS(j), dP(j+1).
+          const uint32_t here = (j & 1) ? kColDP : kColS, there = (j & 1) ? kColS : kColDP;
           if (!(ok = wait(s_done, j & 1))) break;
           tc_fence_after();
-          accumulate(kColAccB, kColS, 32, ring_b(j), j > 0);
-          tc_commit(b_empty(j % kBStages));
           if (more) {
-            product(kColS, L::kFixA, ring_a(j + 1));
+            product(there, L::kFixA, ring_a(j + 1));
             tc_commit(s_full);
-            if (!(ok = wait(b_full((j + 1) % kBStages), ((j + 1) / kBStages) & 1))) break;
           }
-          if (!(ok = wait(ds_full, j & 1))) break;
+          accumulate(kColAccB, here, 32, ring_b(j), j > 0);
+          tc_commit(b_empty(j % kBStages));
+          if (more && !(ok = wait(b_full((j + 1) % kBStages), ((j + 1) / kBStages) & 1))) break;
+          if (!(ok = wait(ds_full(j), (j >> 1) & 1))) break;
           tc_fence_after();
-          accumulate(kColAccA, kColDP, 32, ring_a(j), j > 0);
+          accumulate(kColAccA, here + 32, 32, ring_a(j), j > 0);
           tc_commit(a_empty(j % kAStages));
           if (more) {
-            product(kColDP, L::kFixB, ring_b(j + 1));
+            product(here, L::kFixB, ring_b(j + 1));
             tc_commit(dp_full);
           }
         }
@@ -477,11 +492,11 @@ __device__ __forceinline__ void run_role(const CUtensorMap* tmFixA, const CUtens
     const int row = (warp & 3) * 32 + lane;
     const uint32_t lanes = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
     const bool row_valid = u.block * kT + row < u.S;
-    float row_bias = 0.f, row_delta = 0.f;  // q role: this thread's row
+    float row_bias = 0.f, row_ndelta = 0.f;  // q role: this thread's row
     if (Q) {
       const float* r = p.rows + (static_cast<int64_t>(head) * p.units + u.gqb0 + u.block) * (2 * kT);
       row_bias = r[row];
-      row_delta = r[kT + row];
+      row_ndelta = r[kT + row];
     }
     const float2 c2 = make_float2(p.c2, p.c2);
     bool ok = true;
@@ -495,8 +510,11 @@ __device__ __forceinline__ void run_role(const CUtensorMap* tmFixA, const CUtens
       if (!Q && !(ok = warp_wait(b_full(j % kBStages), (j / kBStages) & 1, abort_flag, p.status))) break;
       if (!(ok = warp_wait(s_full, j & 1, abort_flag, p.status))) break;
       tc_fence_after();
+      // kv role: the two score regions change places with every tile.
+      const uint32_t col_s = lanes + ((Q || !(j & 1)) ? kColS : kColDP) + half * 64;
+      const uint32_t col_dp = lanes + ((Q || !(j & 1)) ? kColDP : kColS) + half * 64;
       uint32_t s[64];
-      tmem_ld_x64_async(lanes + kColS + half * 64, s);
+      tmem_ld_x64_async(col_s, s);
       if (valid < kT) {
         // The tile ends past the sequence. Its rows out there are summation
         // rows of the accumulating products: they must be zeros, not whatever
@@ -514,11 +532,16 @@ __device__ __forceinline__ void run_role(const CUtensorMap* tmFixA, const CUtens
       if (Q) warp_arrive(s_done, lane);
       // P = 2^(c2 S - L log2 e)
 #pragma unroll
-      for (int i = 0; i < 32; ++i) {
-        const float2 bias = Q ? make_float2(row_bias, row_bias) : reinterpret_cast<const float2*>(rows)[i];
-        const float2 e = ffma2(make_float2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), c2, bias);
-        s[2 * i] = __float_as_uint(ex2_approx(e.x));
-        s[2 * i + 1] = __float_as_uint(ex2_approx(e.y));
+      for (int i = 0; i < 16; ++i) {
+        const float4 b4 = Q ? make_float4(row_bias, row_bias, row_bias, row_bias) : reinterpret_cast<const float4*>(rows)[i];
+        const float2 e0 = ffma2(make_float2(__uint_as_float(s[4 * i]), __uint_as_float(s[4 * i + 1])), c2,
+                                make_float2(b4.x, b4.y));
+        const float2 e1 = ffma2(make_float2(__uint_as_float(s[4 * i + 2]), __uint_as_float(s[4 * i + 3])), c2,
+                                make_float2(b4.z, b4.w));
+        s[4 * i] = __float_as_uint(ex2_approx(e0.x));
+        s[4 * i + 1] = __float_as_uint(ex2_approx(e0.y));
+        s[4 * i + 2] = __float_as_uint(ex2_approx(e1.x));
+        s[4 * i + 3] = __float_as_uint(ex2_approx(e1.y));
       }
       if (valid < kT) {  // also where the score of a row past the end was not finite
 #pragma unroll
@@ -529,28 +552,36 @@ __device__ __forceinline__ void run_role(const CUtensorMap* tmFixA, const CUtens
       if (!Q) {
 #pragma unroll
         for (int i = 0; i < 32; ++i) pk[i] = pack_bf16x2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1]));
-        tmem_st_x32(lanes + kColS + half * 64, pk);
-        warp_arrive(s_done, lane);
+        tmem_st_x32(col_s, pk);
       }
       if (!(ok = warp_wait(dp_full, j & 1, abort_flag, p.status))) break;
       tc_fence_after();
       uint32_t d[64];
-      tmem_ld_x64_async(lanes + kColDP + half * 64, d);
+      tmem_ld_x64_async(col_dp, d);
       tmem_wait_ld_tied(d);
-      if (Q) warp_arrive(dp_done, lane);
+      warp_arrive(Q ? dp_done : s_done, lane);
 #pragma unroll
-      for (int i = 0; i < 32; ++i) {
-        const float2 delta = Q ? make_float2(row_delta, row_delta) : reinterpret_cast<const float2*>(rows + kT)[i];
-        float x = __uint_as_float(s[2 * i]) * (__uint_as_float(d[2 * i]) - delta.x);
-        float y = __uint_as_float(s[2 * i + 1]) * (__uint_as_float(d[2 * i + 1]) - delta.y);
-        if (valid < kT) {
-          if (half * 64 + 2 * i >= valid) x = 0.f;
-          if (half * 64 + 2 * i + 1 >= valid) y = 0.f;
-        }
-        pk[i] = pack_bf16x2(x, y);
+      for (int i = 0; i < 16; ++i) {
+        const float4 n4 = Q ? make_float4(row_ndelta, row_ndelta, row_ndelta, row_ndelta)
+                            : reinterpret_cast<const float4*>(rows + kT)[i];
+        const float2 x = fmul2(make_float2(__uint_as_float(s[4 * i]), __uint_as_float(s[4 * i + 1])),
+                               fadd2(make_float2(__uint_as_float(d[4 * i]), __uint_as_float(d[4 * i + 1])),
+                                     make_float2(n4.x, n4.y)));
+        const float2 y = fmul2(make_float2(__uint_as_float(s[4 * i + 2]), __uint_as_float(s[4 * i + 3])),
+                               fadd2(make_float2(__uint_as_float(d[4 * i + 2]), __uint_as_float(d[4 * i + 3])),
+                                     make_float2(n4.z, n4.w)));
+        pk[2 * i] = pack_bf16x2(x.x, x.y);
+        pk[2 * i + 1] = pack_bf16x2(y.x, y.y);
       }
-      tmem_st_x32(lanes + (Q ? kColDS + (j & 1) * 64 + half * 32 : kColDP + half * 64), pk);
-      warp_arrive(ds_full, lane);
+      if (valid < kT) {  // dP past the end may not be finite
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+          const int c = half * 64 + 2 * i;
+          pk[i] = c >= valid ? 0u : (c + 1 >= valid ? pk[i] & 0xFFFFu : pk[i]);
+        }
+      }
+      tmem_st_x32(Q ? lanes + kColDS + (j & 1) * 64 + half * 32 : col_s + 32, pk);
+      warp_arrive(ds_full(j), lane);
     }
 
     // Epilogue: this thread's row and half of the D columns of each accumulator.
@@ -615,7 +646,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(smem_u32(&ctl.dp_full), 1);
     mbar_init(smem_u32(&ctl.s_done), 8);
     mbar_init(smem_u32(&ctl.dp_done), 8);
-    mbar_init(smem_u32(&ctl.ds_full), 8);
+    mbar_init(smem_u32(&ctl.ds_full[0]), 8);
+    mbar_init(smem_u32(&ctl.ds_full[1]), 8);
     mbar_init(smem_u32(&ctl.acc_full), 1);
     mbar_init(smem_u32(&ctl.drain), 1);
     ctl.abort_flag = 0;

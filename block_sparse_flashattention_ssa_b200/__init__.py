@@ -355,6 +355,31 @@ def calibrate_fp8(q8, k8, v, cu_seqlens, max_seqlen: int, q_descale: float, k_de
     return out, counts
 
 
+def _at(t):
+    """Device address of a tensor or None, as ctypes takes it."""
+    return None if t is None else t.data_ptr()
+
+
+def _is(t, dtype, dev, shape):
+    """The checks of _require() that pass in a correct call, in few steps: the
+    calls of a training step are short on the GPU for small batches."""
+    return t.dtype is dtype and t.device == dev and t.shape == shape and t.is_contiguous()
+
+
+def _need(t, name, dtype, dev, shape):
+    """_require() of an argument that must be there."""
+    import torch
+
+    if not (isinstance(t, torch.Tensor) and _is(t, dtype, dev, shape)):
+        _require(t, name, dtype, dev, shape)
+
+
+def _may(t, name, dtype, dev, shape):
+    """_require() of an optional output."""
+    if t is not None:
+        _need(t, name, dtype, dev, shape)
+
+
 def _run(dev, stream, tensors, body):
     """``body(stream handle)`` with ``dev`` current and on ``stream`` (default:
     the device's current one), so that what it allocates belongs to the stream
@@ -363,14 +388,15 @@ def _run(dev, stream, tensors, body):
     import torch
 
     current = torch.cuda.current_stream(dev)
-    if stream is None:
+    here = torch.cuda.current_device() == dev.index
+    if stream is None or (here and stream == current):
+        if here:
+            return body(current.cuda_stream)
         stream = current
     elif stream.device != dev:
         raise ValueError(f"stream is on {stream.device}, the tensors on {dev}")
-    if stream == current and torch.cuda.current_device() == dev.index:
-        return body(ctypes.c_void_p(stream.cuda_stream))
     with torch.cuda.device(dev), torch.cuda.stream(stream):
-        result = body(ctypes.c_void_p(stream.cuda_stream))
+        result = body(stream.cuda_stream)
     if stream != current:
         for t in tensors:
             if t is not None:
@@ -383,15 +409,18 @@ def _run(dev, stream, tensors, body):
 
 def _no_overlap(outputs, inputs):
     """Refuse an output that shares memory with an input or another output
-    (all contiguous): the kernels read and write them in no fixed order."""
-    spans = []
-    for t, name in inputs + outputs:
-        spans.append((t.data_ptr(), t.data_ptr() + t.numel() * t.element_size(), name) if t is not None else None)
-    n = len(inputs)
-    for i, a in enumerate(spans[n:], n):
-        for b in spans[:i]:
-            if a and b and a[0] < b[1] and b[0] < a[1]:
-                raise ValueError(f"{a[2]} overlaps {b[2]}")
+    (all contiguous): the kernels read and write them in no fixed order.
+    Outputs that are None are allocated later and share nothing."""
+    given = [(t, name) for t, name in outputs if t is not None]
+    if not given:
+        return
+    spans = [(t.data_ptr(), t.data_ptr() + t.numel() * t.element_size(), name)
+             for t, name in inputs + given if t is not None]
+    for i in range(len(spans) - len(given), len(spans)):
+        lo, hi, name = spans[i]
+        for other in spans[:i]:
+            if lo < other[1] and other[0] < hi:
+                raise ValueError(f"{name} overlaps {other[2]}")
 
 
 def _check_shared_heads(q, k, v, cu_seqlens, qkv_dtype):
@@ -402,11 +431,11 @@ def _check_shared_heads(q, k, v, cu_seqlens, qkv_dtype):
         raise ValueError("q must be a CUDA tensor")
     total, H, D = _shape(q)
     dev = q.device
-    _require(q, "q", qkv_dtype, dev)
+    _need(q, "q", qkv_dtype, dev, q.shape)
     _require(k, "k", qkv_dtype, dev)
     if k.dim() != 3 or k.shape[0] != total or k.shape[2] != D or k.shape[1] < 1 or H % k.shape[1] != 0:
         raise ValueError(f"k has shape {tuple(k.shape)}, expected [{total}, a divisor of {H}, {D}]")
-    _require(v, "v", qkv_dtype, dev, tuple(k.shape))
+    _need(v, "v", qkv_dtype, dev, k.shape)
     _require(cu_seqlens, "cu_seqlens", torch.int32, dev)
     if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2:
         raise ValueError("cu_seqlens must be a 1-D tensor of batch + 1 offsets")
@@ -424,20 +453,24 @@ def fwd_lse(q, k, v, cu_seqlens, max_seqlen: int, threshold_scale_factor: float 
     import torch
 
     dev, total, H, Hkv, D, batch = _check_shared_heads(q, k, v, cu_seqlens, torch.bfloat16)
-    _require(out, "out", torch.bfloat16, dev, tuple(q.shape), allow_none=True)
-    _require(lse, "lse", torch.float32, dev, (H, total), allow_none=True)
-    nq = _per_unit_qblocks(dev, H, total, batch, _forward_outputs(skip_counter, decision_bitmap, None, max_seqlen))
+    _may(out, "out", torch.bfloat16, dev, q.shape)
+    _may(lse, "lse", torch.float32, dev, (H, total))
+    nq = -1
+    if skip_counter is not None or decision_bitmap is not None:
+        nq = _per_unit_qblocks(dev, H, total, batch, _forward_outputs(skip_counter, decision_bitmap, None, max_seqlen))
     _no_overlap([(out, "out"), (lse, "lse"), (skip_counter, "skip_counter"), (decision_bitmap, "decision_bitmap")],
                 [(q, "q"), (k, "k"), (v, "v"), (cu_seqlens, "cu_seqlens")])
 
     def body(handle):
         o = torch.empty_like(q) if out is None else out
         r = torch.empty((H, total), dtype=torch.float32, device=dev) if lse is None else lse
-        _check(_lib.ssa_fwd_lse(_ptr(q), _ptr(k), _ptr(v), _ptr(cu_seqlens), batch, total, int(max_seqlen), H, Hkv, D,
-                                float(softmax_scale), float(threshold_scale_factor), _ptr(o), _ptr(r),
-                                _ptr(skip_counter), nq, _ptr(decision_bitmap), handle), "ssa_fwd_lse")
+        _check(_lib.ssa_fwd_lse(_at(q), _at(k), _at(v), _at(cu_seqlens), batch, total, max_seqlen, H, Hkv, D,
+                                float(softmax_scale), float(threshold_scale_factor), _at(o), _at(r),
+                                _at(skip_counter), nq,
+                                _at(decision_bitmap), handle), "ssa_fwd_lse")
         return o, r
 
+    max_seqlen = int(max_seqlen)
     return _run(dev, stream, (q, k, v, cu_seqlens, out, lse, skip_counter, decision_bitmap), body)
 
 
@@ -446,18 +479,20 @@ def _backward(what, dout, q, k, v, extra, out, lse, cu_seqlens, max_seqlen, soft
     import torch
 
     dev, total, H, Hkv, D, batch = _check_shared_heads(q, k, v, cu_seqlens, qkv_dtype)
-    bf16, q_shape, k_shape = torch.bfloat16, (total, H, D), (total, Hkv, D)
-    _require(dout, "dout", bf16, dev, q_shape)
-    _require(out, "out", bf16, dev, q_shape)
-    _require(lse, "lse", torch.float32, dev, (H, total))
-    _require(dq, "dq", bf16, dev, q_shape, allow_none=True)
-    _require(dk, "dk", bf16, dev, k_shape, allow_none=True)
-    _require(dv, "dv", bf16, dev, k_shape, allow_none=True)
+    bf16 = torch.bfloat16
+    _need(dout, "dout", bf16, dev, q.shape)
+    _need(out, "out", bf16, dev, q.shape)
+    _need(lse, "lse", torch.float32, dev, (H, total))
+    _may(dq, "dq", bf16, dev, q.shape)
+    _may(dk, "dk", bf16, dev, k.shape)
+    _may(dv, "dv", bf16, dev, k.shape)
     _require(workspace, "workspace", None, dev, allow_none=True)
     for t, name, heads in extra:
-        _require(t, name, torch.float32, dev, ((total + TILE - 1) // TILE, heads))
-    nq = _per_unit_qblocks(dev, H, total, batch, [(decision_bitmap, "decision_bitmap", (torch.int32, torch.uint32),
-                                                    (bitmap_words(max_seqlen),))])
+        _need(t, name, torch.float32, dev, ((total + TILE - 1) // TILE, heads))
+    nq, max_seqlen = -1, int(max_seqlen)
+    if decision_bitmap is not None:
+        nq = _per_unit_qblocks(dev, H, total, batch, [(decision_bitmap, "decision_bitmap", (torch.int32, torch.uint32),
+                                                        (bitmap_words(max_seqlen),))])
     _no_overlap([(dq, "dq"), (dk, "dk"), (dv, "dv"), (workspace, "workspace")],
                 [(dout, "dout"), (q, "q"), (k, "k"), (v, "v"), (out, "out"), (lse, "lse"), (cu_seqlens, "cu_seqlens"),
                  (decision_bitmap, "decision_bitmap")] + [(t, name) for t, name, _ in extra])
@@ -466,13 +501,16 @@ def _backward(what, dout, q, k, v, extra, out, lse, cu_seqlens, max_seqlen, soft
         raise SSAError(int(need), what)
 
     def body(handle):
-        ws = torch.empty(need, dtype=torch.uint8, device=dev) if workspace is None else workspace
-        grads = [torch.empty(shape, dtype=bf16, device=dev) if t is None else t
-                 for t, shape in ((dq, q_shape), (dk, k_shape), (dv, k_shape))]
-        _check(call(_ptr(dout), _ptr(out), _ptr(lse), _ptr(cu_seqlens), batch, total, int(max_seqlen), H, Hkv, D,
-                    float(softmax_scale), _ptr(decision_bitmap), nq, *[_ptr(g) for g in grads], _ptr(ws),
-                    ws.numel() * ws.element_size(), handle), what)
-        return tuple(grads)
+        if workspace is None:
+            ws, size = torch.empty(need, dtype=torch.uint8, device=dev), need
+        else:
+            ws, size = workspace, workspace.numel() * workspace.element_size()
+        gq = torch.empty_like(out) if dq is None else dq
+        gk = torch.empty_like(k, dtype=bf16) if dk is None else dk
+        gv = torch.empty_like(gk) if dv is None else dv
+        _check(call(_at(dout), _at(out), _at(lse), _at(cu_seqlens), batch, total, max_seqlen, H, Hkv, D,
+                    float(softmax_scale), _at(decision_bitmap), nq, _at(gq), _at(gk), _at(gv), _at(ws), size, handle), what)
+        return gq, gk, gv
 
     return _run(dev, stream, (dout, q, k, v, out, lse, cu_seqlens, decision_bitmap, dq, dk, dv, workspace)
                 + tuple(t for t, _, _ in extra), body)
@@ -491,7 +529,7 @@ def bwd(dout, q, k, v, out, lse, cu_seqlens, max_seqlen: int, softmax_scale: flo
     return _backward(
         "ssa_bwd", dout, q, k, v, [], out, lse, cu_seqlens, max_seqlen, softmax_scale, decision_bitmap, dq, dk, dv,
         workspace, stream, torch.bfloat16, lambda total, batch, H, Hkv, D: _lib.ssa_bwd_workspace_bytes(total, batch, H),
-        lambda g, *rest: _lib.ssa_bwd(g, _ptr(q), _ptr(k), _ptr(v), *rest))
+        lambda g, *rest: _lib.ssa_bwd(g, _at(q), _at(k), _at(v), *rest))
 
 
 def bwd_fp8(dout, q_saved, k_saved, v_saved, out, lse, cu_seqlens, max_seqlen: int, softmax_scale: float = 0.0,
@@ -506,7 +544,7 @@ def bwd_fp8(dout, q_saved, k_saved, v_saved, out, lse, cu_seqlens, max_seqlen: i
         "ssa_bwd_fp8", dout, q, k, v, [(qs, "q_scales", heads(q)), (ks, "k_scales", heads(k)), (vs, "v_scales", heads(v))],
         out, lse, cu_seqlens, max_seqlen, softmax_scale, decision_bitmap, dq, dk, dv, workspace, stream, torch.uint8,
         _lib.ssa_bwd_fp8_workspace_bytes,
-        lambda g, *rest: _lib.ssa_bwd_fp8(g, _ptr(q), _ptr(qs), _ptr(k), _ptr(ks), _ptr(v), _ptr(vs), *rest))
+        lambda g, *rest: _lib.ssa_bwd_fp8(g, _at(q), _at(qs), _at(k), _at(ks), _at(v), _at(vs), *rest))
 
 
 def bwd_workspace_bytes(total_tokens: int, batch: int, num_heads: int) -> int:
@@ -537,15 +575,15 @@ def save_fp8(x, codes=None, scales=None, stream=None):
         raise ValueError("x must be a CUDA tensor")
     total, H, D = _shape(x)
     dev, s_shape = x.device, ((total + TILE - 1) // TILE, H)
-    _require(x, "x", torch.bfloat16, dev)
-    _require(codes, "codes", torch.uint8, dev, tuple(x.shape), allow_none=True)
-    _require(scales, "scales", torch.float32, dev, s_shape, allow_none=True)
+    _need(x, "x", torch.bfloat16, dev, x.shape)
+    _may(codes, "codes", torch.uint8, dev, x.shape)
+    _may(scales, "scales", torch.float32, dev, s_shape)
     _no_overlap([(codes, "codes"), (scales, "scales")], [(x, "x")])
 
     def body(handle):
-        c = torch.empty(x.shape, dtype=torch.uint8, device=dev) if codes is None else codes
+        c = torch.empty_like(x, dtype=torch.uint8) if codes is None else codes
         s = torch.empty(s_shape, dtype=torch.float32, device=dev) if scales is None else scales
-        _check(_lib.ssa_save_fp8(_ptr(x), _ptr(c), _ptr(s), total, H, D, handle), "ssa_save_fp8")
+        _check(_lib.ssa_save_fp8(_at(x), _at(c), _at(s), total, H, D, handle), "ssa_save_fp8")
         return c, s
 
     return _run(dev, stream, (x, codes, scales), body)
@@ -559,14 +597,14 @@ def restore_fp8(codes, scales, out=None, stream=None):
         raise ValueError("codes must be a CUDA tensor")
     total, H, D = _shape(codes)
     dev = codes.device
-    _require(codes, "codes", torch.uint8, dev)
-    _require(scales, "scales", torch.float32, dev, ((total + TILE - 1) // TILE, H))
-    _require(out, "out", torch.bfloat16, dev, tuple(codes.shape), allow_none=True)
+    _need(codes, "codes", torch.uint8, dev, codes.shape)
+    _need(scales, "scales", torch.float32, dev, ((total + TILE - 1) // TILE, H))
+    _may(out, "out", torch.bfloat16, dev, codes.shape)
     _no_overlap([(out, "out")], [(codes, "codes"), (scales, "scales")])
 
     def body(handle):
-        x = torch.empty(codes.shape, dtype=torch.bfloat16, device=dev) if out is None else out
-        _check(_lib.ssa_restore_fp8(_ptr(codes), _ptr(scales), _ptr(x), total, H, D, handle), "ssa_restore_fp8")
+        x = torch.empty_like(codes, dtype=torch.bfloat16) if out is None else out
+        _check(_lib.ssa_restore_fp8(_at(codes), _at(scales), _at(x), total, H, D, handle), "ssa_restore_fp8")
         return (x,)
 
     return _run(dev, stream, (codes, scales, out), body)[0]
@@ -579,14 +617,18 @@ def _rows(t, name, dev, total, dim):
 
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.device != dev or t.dtype != torch.bfloat16:
+    if t.dtype is not torch.bfloat16 or t.device != dev:
         raise ValueError(f"{name} is {t.dtype} on {t.device}, expected torch.bfloat16 on {dev}")
-    if t.dim() != 3 or t.shape[0] != total or t.shape[2] != dim:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected [{total}, heads, {dim}]")
-    H = t.shape[1]
-    if (dim > 1 and t.stride(2) != 1) or (H > 1 and t.stride(1) != dim) or (total > 1 and t.stride(0) < H * dim):
+    shape = t.shape
+    if len(shape) != 3 or shape[0] != total or shape[2] != dim:
+        raise ValueError(f"{name} has shape {tuple(shape)}, expected [{total}, heads, {dim}]")
+    row = shape[1] * dim
+    if t.is_contiguous():
+        return row
+    s0, s1, s2 = t.stride()
+    if (dim > 1 and s2 != 1) or (shape[1] > 1 and s1 != dim) or (total > 1 and s0 < row):
         raise ValueError(f"{name}: the heads of a token must be contiguous and tokens must not overlap")
-    return t.stride(0) if total > 1 else H * dim
+    return s0 if total > 1 else row
 
 
 def _rows_overlap(a, a_stride, b, b_stride):
@@ -619,18 +661,21 @@ def rotary(q, k, positions, inv_freq, sections=None, interleaved: bool = False, 
         raise ValueError("q must be a CUDA tensor")
     total, H, D = _shape(q)
     dev = q.device
-    _require(positions, "positions", torch.int32, dev)
+    if not (isinstance(positions, torch.Tensor) and _is(positions, torch.int32, dev, positions.shape)):
+        _require(positions, "positions", torch.int32, dev)
     axes = 1 if positions.dim() == 1 else positions.shape[-1]
-    if tuple(positions.shape) not in ((total,), (total, axes)):
+    if positions.shape != ((total,) if positions.dim() == 1 else (total, axes)):
         raise ValueError(f"positions has shape {tuple(positions.shape)}, expected [{total}] or [{total}, axes]")
-    _require(inv_freq, "inv_freq", torch.float64, dev)
-    if inv_freq.dim() != 1 or 2 * inv_freq.numel() > D:
+    if not (isinstance(inv_freq, torch.Tensor) and _is(inv_freq, torch.float64, dev, inv_freq.shape)):
+        _require(inv_freq, "inv_freq", torch.float64, dev)
+    pairs = inv_freq.numel()
+    if inv_freq.dim() != 1 or 2 * pairs > D:
         raise ValueError(f"inv_freq must be 1-D with at most {D // 2} frequencies")
     if sections is None and axes > 1:
         raise ValueError("sections must say how many pairs turn with each of the position axes")
-    counts = [inv_freq.numel()] if sections is None else [int(n) for n in sections]
-    if len(counts) != axes or min(counts) < 0 or sum(counts) != inv_freq.numel():
-        raise ValueError(f"sections must be {axes} counts adding up to {inv_freq.numel()}")
+    counts = [pairs] if sections is None else [int(n) for n in sections]
+    if len(counts) != axes or min(counts) < 0 or sum(counts) != pairs:
+        raise ValueError(f"sections must be {axes} counts adding up to {pairs}")
     Hk = 0 if k is None else k.shape[1]
     xs = [_rows(q, "q", dev, total, D), 0 if k is None else _rows(k, "k", dev, total, D)]
     ys = [H * D, Hk * D]
@@ -654,11 +699,11 @@ def rotary(q, k, positions, inv_freq, sections=None, interleaved: bool = False, 
     n_pairs = (ctypes.c_int32 * axes)(*counts)
 
     def body(handle):
-        oq = torch.empty((total, H, D), dtype=torch.bfloat16, device=dev) if out_q is None else out_q
-        ok = torch.empty((total, Hk, D), dtype=torch.bfloat16, device=dev) if out_k is None and Hk else out_k
-        _check(_lib.ssa_rotary(_ptr(q), _ptr(k), _ptr(oq), _ptr(ok), xs[0], xs[1], ys[0], ys[1], total, H, Hk, D,
-                               _ptr(positions), axes, n_pairs, _ptr(inv_freq), 2 * inv_freq.numel(),
-                               1 if interleaved else 0, float(scale), 1 if transpose else 0, handle), "ssa_rotary")
+        oq = torch.empty_like(q, memory_format=torch.contiguous_format) if out_q is None else out_q
+        ok = torch.empty_like(k, memory_format=torch.contiguous_format) if out_k is None and Hk else out_k
+        _check(_lib.ssa_rotary(_at(q), _at(k), _at(oq), _at(ok), xs[0], xs[1], ys[0], ys[1], total, H, Hk, D,
+                               _at(positions), axes, n_pairs, _at(inv_freq), 2 * pairs, 1 if interleaved else 0,
+                               float(scale), 1 if transpose else 0, handle), "ssa_rotary")
         return oq, ok
 
     return _run(dev, stream, (q, k, positions, inv_freq, out_q, out_k), body)

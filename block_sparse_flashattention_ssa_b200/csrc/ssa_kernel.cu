@@ -959,25 +959,22 @@ struct Call {
   float* lse = nullptr;         // row log-sum-exp output (LSE only)
 };
 
-// True when `p` is device (or managed) memory of the current device: a host
-// pointer handed to a kernel or a tensor map would fault the GPU, so every
-// pointer the kernels touch is checked before a launch.
-bool on_current_device(const void* ptr) {
-  if (!ptr) return false;
-  int dev = -1;
-  if (cudaGetDevice(&dev) != cudaSuccess) return false;
-  cudaPointerAttributes attr{};
-  if (cudaPointerGetAttributes(&attr, ptr) != cudaSuccess) {
-    cudaGetLastError();  // clear the error this query may leave behind
-    return false;
-  }
-  return (attr.type == cudaMemoryTypeDevice || attr.type == cudaMemoryTypeManaged) && attr.device == dev;
-}
-
-// Every non-null pointer of `ptrs` lives on the current device.
+// Every non-null pointer of `ptrs` is device (or managed) memory of the
+// current device: a host pointer handed to a kernel or a tensor map would
+// fault the GPU, so every pointer the kernels touch is checked before a launch.
 int check_device_pointers(std::initializer_list<const void*> ptrs) {
-  for (const void* ptr : ptrs)
-    if (ptr && !on_current_device(ptr)) return SSA_ERR_INVALID_ARG;
+  int dev = -1;
+  for (const void* ptr : ptrs) {
+    if (!ptr) continue;
+    if (dev < 0 && cudaGetDevice(&dev) != cudaSuccess) return SSA_ERR_INVALID_ARG;
+    cudaPointerAttributes attr{};
+    if (cudaPointerGetAttributes(&attr, ptr) != cudaSuccess) {
+      cudaGetLastError();  // clear the error this query may leave behind
+      return SSA_ERR_INVALID_ARG;
+    }
+    if ((attr.type != cudaMemoryTypeDevice && attr.type != cudaMemoryTypeManaged) || attr.device != dev)
+      return SSA_ERR_INVALID_ARG;
+  }
   return SSA_OK;
 }
 

@@ -51,13 +51,62 @@ __device__ __forceinline__ uint32_t pack(float lo, float hi) {
 __device__ __forceinline__ float low(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float high(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 
-// VEC: the heads are made of 16-byte pieces and, in the half layout, so is half
-// the rotated part, so that a thread turns 8 elements (interleaved) or 8 pairs
-// (half) with 16-byte accesses; otherwise one element or pair at a time.
-template <bool INTERLEAVED, bool VEC>
-__global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant__ Params p, int tokens_per_cta) {
-  extern __shared__ float2 table[];  // [tokens_per_cta][rot / 2]
+// N consecutive elements of a head, moved with one access of 2 N bytes.
+template <int N>
+struct Piece;
+template <>
+struct Piece<8> {
+  uint32_t w[4];
+  __device__ __forceinline__ void load(const __nv_bfloat16* x) {
+    const uint4 v = __ldcs(reinterpret_cast<const uint4*>(x));
+    w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+  }
+  __device__ __forceinline__ void store(__nv_bfloat16* y) const {
+    __stcs(reinterpret_cast<uint4*>(y), make_uint4(w[0], w[1], w[2], w[3]));
+  }
+};
+template <>
+struct Piece<4> {
+  uint32_t w[2];
+  __device__ __forceinline__ void load(const __nv_bfloat16* x) {
+    const uint2 v = __ldcs(reinterpret_cast<const uint2*>(x));
+    w[0] = v.x, w[1] = v.y;
+  }
+  __device__ __forceinline__ void store(__nv_bfloat16* y) const { __stcs(reinterpret_cast<uint2*>(y), make_uint2(w[0], w[1])); }
+};
+template <>
+struct Piece<2> {
+  uint32_t w[1];
+  __device__ __forceinline__ void load(const __nv_bfloat16* x) { w[0] = __ldcs(reinterpret_cast<const uint32_t*>(x)); }
+  __device__ __forceinline__ void store(__nv_bfloat16* y) const { __stcs(reinterpret_cast<uint32_t*>(y), w[0]); }
+};
+template <>
+struct Piece<1> {  // in the low half of the word
+  uint32_t w[1];
+  __device__ __forceinline__ void load(const __nv_bfloat16* x) { w[0] = __ldcs(reinterpret_cast<const unsigned short*>(x)); }
+  __device__ __forceinline__ void store(__nv_bfloat16* y) const {
+    __stcs(reinterpret_cast<unsigned short*>(y), static_cast<unsigned short>(w[0]));
+  }
+};
+
+// A piece is what one thread takes of a head at a time:
+//   interleaved  N = 8 elements (4 pairs; the last one may hold copied
+//                elements as well), or one pair as two single elements when the
+//                rows are not 16-byte aligned (N = 1);
+//   half         N pairs, as two runs of N elements, or N copied elements; N is
+//                the largest of 8, 4, 2, 1 that divides rot / 2 and suits the
+//                rows' alignment.
+// A thread keeps its piece and steps through the CTA's rows (token, head of Q
+// then K) kBatch at a time, all loads of a batch first. The table of (cos,
+// sin) holds two pairs to a float4, the k-th float4 of all pieces side by
+// side, so that a warp reads it without bank conflicts.
+template <bool INTERLEAVED, int N>
+__global__ void __launch_bounds__(kThreads, 4) rotary_kernel(const __grid_constant__ Params p, int tokens_per_cta) {
+  extern __shared__ __align__(16) float2 table[];  // [tokens_per_cta][turned * kPairs]
+  constexpr int kPairs = INTERLEAVED ? (N == 8 ? 4 : 1) : N;  // pairs of a piece
+  constexpr int kCopied = INTERLEAVED && N == 8 ? 8 : N;      // elements of a copied piece
   const int pairs = p.rot / 2;
+  const int turned = (pairs + kPairs - 1) / kPairs, row_table = turned * kPairs;
   const int64_t t0 = static_cast<int64_t>(blockIdx.x) * tokens_per_cta;
   const int nt = static_cast<int>(min(static_cast<int64_t>(tokens_per_cta), p.tokens - t0));
   for (int i = threadIdx.x; i < nt * pairs; i += kThreads) {
@@ -68,86 +117,92 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant_
     const double turns = pos * (p.inv_freq[j] * 0.15915494309189533577);  // 1 / 2 pi
     float s, c;
     sincospif(2.f * static_cast<float>(turns - rint(turns)), &s, &c);
-    table[i] = make_float2(c * p.scale, s * p.scale * p.sign);
+    const int piece = j / kPairs, k = j % kPairs;
+    const int at = kPairs == 1 ? j : ((k / 2) * turned + piece) * 2 + (k & 1);
+    table[t * row_table + at] = make_float2(c * p.scale, s * p.scale * p.sign);
   }
   __syncthreads();
 
-  // A piece is what one thread turns at a time; a head has `turned` of them
-  // and then `rest` copied ones.
-  const int step = VEC ? 8 : 1;
-  const int turned = INTERLEAVED ? (VEC ? p.rot / 8 : pairs) : pairs / step;
-  const int rest = (p.dim - p.rot) / step;
-  const int pieces = turned + rest;
-  const int per_token = (p.heads[0] + p.heads[1]) * pieces;
-  for (int i = threadIdx.x; i < nt * per_token; i += kThreads) {
-    const int t = i / per_token;
-    int r = i - t * per_token;
-    const int head_all = r / pieces, piece = r - head_all * pieces;
-    const int which = head_all >= p.heads[0] ? 1 : 0;
-    const int head = head_all - (which ? p.heads[0] : 0);
-    const __nv_bfloat16* x = p.x[which] + (t0 + t) * p.xs[which] + static_cast<int64_t>(head) * p.dim;
-    __nv_bfloat16* y = p.y[which] + (t0 + t) * p.ys[which] + static_cast<int64_t>(head) * p.dim;
-    const float2* cs = table + t * pairs;
-    if (piece >= turned) {
-      const int at = p.rot + (piece - turned) * step;
-      if (VEC)
-        *reinterpret_cast<uint4*>(y + at) = *reinterpret_cast<const uint4*>(x + at);
-      else
-        y[at] = x[at];
-    } else if (INTERLEAVED) {
-      if (VEC) {
-        const uint4 v = *reinterpret_cast<const uint4*>(x + piece * 8);
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-        uint32_t o[4];
+  const int first_copied = INTERLEAVED && N == 8 ? turned * 8 : p.rot;
+  const int pieces = turned + (p.dim - first_copied) / kCopied;  // at most 256
+  const int stride = kThreads / pieces;                          // rows the CTA takes at once
+  const int piece = static_cast<int>(threadIdx.x) % pieces;
+  int row = static_cast<int>(threadIdx.x) / pieces;
+  if (row >= stride) return;
+  const int heads = p.heads[0] + p.heads[1];
+  const bool copy = piece >= turned;
+  const int at = copy ? first_copied + (piece - turned) * kCopied : (INTERLEAVED ? piece * 2 * kPairs : piece * N);
+  const int at2 = INTERLEAVED ? at + 1 : at + pairs;  // the other elements of the pairs, where they stand apart
+  constexpr bool kApart = !(INTERLEAVED && N == 8);
+  constexpr int kBatch = N == 8 ? (INTERLEAVED ? 4 : 2) : 4;
+  int token = row / heads, head = row - token * heads;
+  while (token < nt) {
+    __nv_bfloat16* y[kBatch];
+    const float2* cs[kBatch];
+    Piece<N> a[kBatch], b[kBatch];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          float a, b;
-          turn_pair(low(w[k]), high(w[k]), cs[piece * 4 + k], a, b);
-          o[k] = pack(a, b);
+    for (int i = 0; i < kBatch; ++i) {
+      const int which = head >= p.heads[0] ? 1 : 0;
+      const int64_t h = static_cast<int64_t>(head - (which ? p.heads[0] : 0)) * p.dim;
+      const __nv_bfloat16* x = p.x[which] + (t0 + token) * p.xs[which] + h;
+      y[i] = token < nt ? p.y[which] + (t0 + token) * p.ys[which] + h : nullptr;
+      cs[i] = table + token * row_table;
+      if (token < nt) {
+        a[i].load(x + at);
+        if (kApart && !copy) b[i].load(x + at2);
+      }
+      head += stride;
+      while (head >= heads) {
+        head -= heads;
+        ++token;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      if (!y[i]) continue;
+      if (!copy) {
+        if (kPairs == 1) {
+          float lo, hi;
+          turn_pair(low(a[i].w[0]), low(b[i].w[0]), cs[i][piece], lo, hi);
+          a[i].w[0] = pack(lo, 0.f);
+          b[i].w[0] = pack(hi, 0.f);
+        } else {
+#pragma unroll
+          for (int k = 0; k < kPairs; k += 2) {
+            const float4 c2 = reinterpret_cast<const float4*>(cs[i])[(k / 2) * turned + piece];
+            const float2 c0 = make_float2(c2.x, c2.y), c1 = make_float2(c2.z, c2.w);
+            float l0, h0, l1, h1;
+            if (kApart) {
+              uint32_t &wa = a[i].w[k / 2], &wb = b[i].w[k / 2];
+              turn_pair(low(wa), low(wb), c0, l0, h0);
+              turn_pair(high(wa), high(wb), c1, l1, h1);
+              wa = pack(l0, l1);
+              wb = pack(h0, h1);
+            } else {  // the piece across the end of the rotated part keeps its other elements
+              uint32_t &w0 = a[i].w[k], &w1 = a[i].w[k + 1];
+              turn_pair(low(w0), high(w0), c0, l0, h0);
+              turn_pair(low(w1), high(w1), c1, l1, h1);
+              if (piece * kPairs + k < pairs) w0 = pack(l0, h0);
+              if (piece * kPairs + k + 1 < pairs) w1 = pack(l1, h1);
+            }
+          }
         }
-        *reinterpret_cast<uint4*>(y + piece * 8) = make_uint4(o[0], o[1], o[2], o[3]);
-      } else {
-        float a, b;
-        turn_pair(__bfloat162float(x[2 * piece]), __bfloat162float(x[2 * piece + 1]), cs[piece], a, b);
-        y[2 * piece] = __float2bfloat16_rn(a);
-        y[2 * piece + 1] = __float2bfloat16_rn(b);
+        if (kApart) b[i].store(y[i] + at2);
       }
-    } else if (VEC) {
-      const uint4 va = *reinterpret_cast<const uint4*>(x + piece * 8);
-      const uint4 vb = *reinterpret_cast<const uint4*>(x + pairs + piece * 8);
-      const uint32_t wa[4] = {va.x, va.y, va.z, va.w}, wb[4] = {vb.x, vb.y, vb.z, vb.w};
-      uint32_t oa[4], ob[4];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        float a0, b0, a1, b1;
-        turn_pair(low(wa[k]), low(wb[k]), cs[piece * 8 + 2 * k], a0, b0);
-        turn_pair(high(wa[k]), high(wb[k]), cs[piece * 8 + 2 * k + 1], a1, b1);
-        oa[k] = pack(a0, a1);
-        ob[k] = pack(b0, b1);
-      }
-      *reinterpret_cast<uint4*>(y + piece * 8) = make_uint4(oa[0], oa[1], oa[2], oa[3]);
-      *reinterpret_cast<uint4*>(y + pairs + piece * 8) = make_uint4(ob[0], ob[1], ob[2], ob[3]);
-    } else {
-      float a, b;
-      turn_pair(__bfloat162float(x[piece]), __bfloat162float(x[pairs + piece]), cs[piece], a, b);
-      y[piece] = __float2bfloat16_rn(a);
-      y[pairs + piece] = __float2bfloat16_rn(b);
+      a[i].store(y[i] + at);
     }
   }
 }
 
-template <bool INTERLEAVED>
-int launch(const Params& p, bool vec, cudaStream_t stream) {
-  // Enough tokens per CTA that its threads have about four pieces each.
+template <bool INTERLEAVED, int N>
+int launch(const Params& p, cudaStream_t stream) {
+  // Enough tokens per CTA that a thread has two batches of 16-byte pieces.
   const int per_token = (p.heads[0] + p.heads[1]) * (p.dim / 8);
-  int n = (4 * kThreads + per_token - 1) / per_token;
+  int n = (8 * kThreads + per_token - 1) / per_token;
   n = n < 1 ? 1 : (n > 16 ? 16 : n);
   const unsigned blocks = static_cast<unsigned>((static_cast<int64_t>(p.tokens) + n - 1) / n);
-  const size_t smem = static_cast<size_t>(n) * (p.rot / 2) * sizeof(float2);
-  if (vec)
-    rotary_kernel<INTERLEAVED, true><<<blocks, kThreads, smem, stream>>>(p, n);
-  else
-    rotary_kernel<INTERLEAVED, false><<<blocks, kThreads, smem, stream>>>(p, n);
+  const size_t smem = static_cast<size_t>(n) * (p.rot / 2 + 3) * sizeof(float2);  // + 3: the last piece's unused pairs
+  rotary_kernel<INTERLEAVED, N><<<blocks, kThreads, smem, stream>>>(p, n);
   const cudaError_t e = cudaGetLastError();
   return e == cudaSuccess ? SSA_OK : internal::fail(e);
 }
@@ -188,18 +243,20 @@ extern "C" int ssa_rotary(const void* q, const void* k, void* q_out, void* k_out
   const void* in[2] = {q, k};
   void* out[2] = {q_out, k_out};
   const int64_t xs[2] = {q_stride, k_stride}, ys[2] = {q_out_stride, k_out_stride};
-  bool vec = interleaved ? rotary_dim % 8 == 0 : (rotary_dim / 2) % 8 == 0;
+  // Largest run of elements, up to 8, that suits every address and stride and,
+  // in the half layout, the distance between the elements of a pair.
+  uint64_t steps = 8 | (interleaved ? 0 : static_cast<uint64_t>(rotary_dim / 2));
   for (int i = 0; i < n; ++i) {
-    if ((reinterpret_cast<uintptr_t>(in[i]) | reinterpret_cast<uintptr_t>(out[i])) & 1u) return SSA_ERR_UNSUPPORTED;
-    if (((reinterpret_cast<uintptr_t>(in[i]) | reinterpret_cast<uintptr_t>(out[i])) & 15u) || xs[i] % 8 != 0 ||
-        ys[i] % 8 != 0)
-      vec = false;
+    const uintptr_t both = reinterpret_cast<uintptr_t>(in[i]) | reinterpret_cast<uintptr_t>(out[i]);
+    if (both & 1u) return SSA_ERR_UNSUPPORTED;
+    steps |= both / 2 | static_cast<uint64_t>(xs[i]) | static_cast<uint64_t>(ys[i]);
     p.x[i] = static_cast<const __nv_bfloat16*>(in[i]);
     p.y[i] = static_cast<__nv_bfloat16*>(out[i]);
     p.xs[i] = xs[i];
     p.ys[i] = ys[i];
     p.heads[i] = i ? num_kv_heads : num_heads;
   }
+  steps &= ~steps + 1;  // its lowest set bit
   if (const int rc = internal::device_pointers({q, q_out, positions, rotary_dim > 0 ? inv_freq : nullptr,
                                                 n == 2 ? k : nullptr, n == 2 ? k_out : nullptr});
       rc != SSA_OK)
@@ -212,6 +269,12 @@ extern "C" int ssa_rotary(const void* q, const void* k, void* q_out, void* k_out
   p.rot = rotary_dim;
   p.scale = scale;
   p.sign = transpose ? -1.f : 1.f;
-  return interleaved ? launch<true>(p, vec, static_cast<cudaStream_t>(stream))
-                     : launch<false>(p, vec, static_cast<cudaStream_t>(stream));
+  const cudaStream_t on = static_cast<cudaStream_t>(stream);
+  if (interleaved) return steps == 8 ? launch<true, 8>(p, on) : launch<true, 1>(p, on);
+  switch (steps) {
+    case 8: return launch<false, 8>(p, on);
+    case 4: return launch<false, 4>(p, on);
+    case 2: return launch<false, 2>(p, on);
+    default: return launch<false, 1>(p, on);
+  }
 }

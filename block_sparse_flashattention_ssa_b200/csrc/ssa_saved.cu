@@ -39,28 +39,49 @@ __global__ void __launch_bounds__(kThreads) save_kernel(const __nv_bfloat16* __r
   const int64_t base = (t0 * heads + head) * D + part * 8;
   const int rows = static_cast<int>(min(static_cast<int64_t>(kT), tokens - t0));
   uint4 v[kSteps];
-  uint32_t top = 0;  // largest finite |x| as bf16 bits in the upper half (orders like the value)
 #pragma unroll
   for (int i = 0; i < kSteps; ++i) {
     const int r = r0 + i * kRowsAtOnce;
-    v[i] = r < rows ? *reinterpret_cast<const uint4*>(x + base + static_cast<int64_t>(r) * heads * D)
+    v[i] = r < rows ? __ldcs(reinterpret_cast<const uint4*>(x + base + static_cast<int64_t>(r) * heads * D))
                     : make_uint4(0, 0, 0, 0);
   }
+  // Largest |x|, two at a time; the packed maximum passes over NaN, not over
+  // infinities, which are rare enough for a second look.
+  __nv_bfloat162 top2 = __floats2bfloat162_rn(0.f, 0.f);
 #pragma unroll
   for (int i = 0; i < kSteps; ++i) {
     const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      const uint32_t lo = (w[k] << 16) & 0x7FFF0000u, hi = w[k] & 0x7FFF0000u;
-      top = max(top, lo < 0x7F800000u ? lo : 0u);
-      top = max(top, hi < 0x7F800000u ? hi : 0u);
+      const uint32_t a = w[k] & 0x7FFF7FFFu;
+      top2 = __hmax2(top2, *reinterpret_cast<const __nv_bfloat162*>(&a));
     }
   }
-  top = __reduce_max_sync(0xFFFFFFFFu, top);
-  if ((threadIdx.x & 31) == 0) warp_max[threadIdx.x >> 5] = top;
-  __syncthreads();
+  auto widest = [&](uint32_t t) -> uint32_t {  // over the CTA, as fp32 bits (which order like the values)
+    t = __reduce_max_sync(0xFFFFFFFFu, t);
+    if ((threadIdx.x & 31) == 0) warp_max[threadIdx.x >> 5] = t;
+    __syncthreads();
 #pragma unroll
-  for (int i = 0; i < kThreads / 32; ++i) top = max(top, warp_max[i]);
+    for (int i = 0; i < kThreads / 32; ++i) t = max(t, warp_max[i]);
+    return t;
+  };
+  const uint32_t pair = *reinterpret_cast<const uint32_t*>(&top2);
+  uint32_t top = widest(max(pair << 16, pair & 0xFFFF0000u));
+  const bool infinite = top >= 0x7F800000u;  // uniform
+  if (infinite) {
+    uint32_t t = 0;
+#pragma unroll
+    for (int i = 0; i < kSteps; ++i) {
+      const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const uint32_t lo = (w[k] << 16) & 0x7FFF0000u, hi = w[k] & 0x7FFF0000u;
+        t = max(t, max(lo < 0x7F800000u ? lo : 0u, hi < 0x7F800000u ? hi : 0u));
+      }
+    }
+    __syncthreads();
+    top = widest(t);
+  }
   // |x| = m 2^k with 1 <= m < 2 is at most 448 s = 1.75 2^8 s when s = 2^(k-8)
   // and m <= 1.75, else s = 2^(k-7). Subnormal maxima fall below the least scale.
   int e = static_cast<int>(top >> 23) - 127 - 8 + ((top & 0x7FFFFFu) > 0x600000u ? 1 : 0);
@@ -76,8 +97,10 @@ __global__ void __launch_bounds__(kThreads) save_kernel(const __nv_bfloat16* __r
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       float lo = __uint_as_float(w[k] << 16) * inv, hi = __uint_as_float(w[k] & 0xFFFF0000u) * inv;
-      if (isinf(lo)) lo = __int_as_float(0x7FC00000);
-      if (isinf(hi)) hi = __int_as_float(0x7FC00000);
+      if (infinite) {
+        if (isinf(lo)) lo = __int_as_float(0x7FC00000);
+        if (isinf(hi)) hi = __int_as_float(0x7FC00000);
+      }
       o[k >> 1] |= sm100::pack_e4m3x2(lo, hi) << ((k & 1) * 16);
     }
     if (r < rows)
@@ -104,28 +127,40 @@ struct Restore {
   int tokens;
 };
 
-// Eight elements per thread; blockIdx.y is the tensor.
+constexpr int kPieces = 8;  // 8-element pieces per thread: loads of all of them go out first
+
+// blockIdx.x: block of 128 tokens; blockIdx.y: kThreads * kPieces of its
+// 8-element pieces; blockIdx.z: the tensor.
 template <int D>
 __global__ void __launch_bounds__(kThreads) restore_kernel(const __grid_constant__ Restore p) {
-  const int z = blockIdx.y;
-  const int per_row = p.heads[z] * (D / 8);
-  const int64_t n = static_cast<int64_t>(p.tokens) * per_row;
-  const uint2* __restrict__ codes = reinterpret_cast<const uint2*>(p.codes[z]);
-  uint4* __restrict__ x = reinterpret_cast<uint4*>(p.x[z]);
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; i < n;
-       i += static_cast<int64_t>(gridDim.x) * kThreads) {
-    const int64_t t = i / per_row;
-    const int head = static_cast<int>(i - t * per_row) / (D / 8);
-    const float s = p.scales[z][(t / kT) * p.heads[z] + head];
-    const uint2 c = codes[i];
-    const uint32_t w[4] = {c.x & 0xFFFFu, c.x >> 16, c.y & 0xFFFFu, c.y >> 16};
-    uint32_t o[4];
+  const int z = blockIdx.z;
+  const int heads = p.heads[z], per_row = heads * (D / 8);
+  const int64_t t0 = static_cast<int64_t>(blockIdx.x) * kT;
+  const int n = static_cast<int>(min(static_cast<int64_t>(kT), p.tokens - t0)) * per_row;  // pieces of the block
+  const int first = static_cast<int>(blockIdx.y) * (kThreads * kPieces) + static_cast<int>(threadIdx.x);
+  if (first >= n) return;
+  const uint2* codes = reinterpret_cast<const uint2*>(p.codes[z]) + t0 * per_row + first;
+  uint4* x = reinterpret_cast<uint4*>(p.x[z]) + t0 * per_row + first;
+  const float* scales = p.scales[z] + static_cast<int64_t>(blockIdx.x) * heads;
+  uint2 v[kPieces];
+  float s[kPieces];
+  int col = first % per_row;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const float2 f = decode2(w[k]);
-      o[k] = sm100::pack_bf16x2(f.x * s, f.y * s);
+  for (int i = 0; i < kPieces; ++i) {
+    if (first + i * kThreads < n) {
+      v[i] = __ldcs(codes + i * kThreads);
+      s[i] = scales[col / (D / 8)];
     }
-    x[i] = make_uint4(o[0], o[1], o[2], o[3]);
+    col += kThreads;
+    while (col >= per_row) col -= per_row;
+  }
+#pragma unroll
+  for (int i = 0; i < kPieces; ++i) {
+    if (first + i * kThreads >= n) break;
+    const float2 a = decode2(v[i].x & 0xFFFFu), b = decode2(v[i].x >> 16);
+    const float2 c = decode2(v[i].y & 0xFFFFu), d = decode2(v[i].y >> 16);
+    x[i * kThreads] = make_uint4(sm100::pack_bf16x2(a.x * s[i], a.y * s[i]), sm100::pack_bf16x2(b.x * s[i], b.y * s[i]),
+                                 sm100::pack_bf16x2(c.x * s[i], c.y * s[i]), sm100::pack_bf16x2(d.x * s[i], d.y * s[i]));
   }
 }
 
@@ -134,7 +169,7 @@ int check(const void* codes, const float* scales, const void* x, int tokens, int
   if (dim != 64 && dim != 128) return SSA_ERR_UNSUPPORTED;
   if (tokens == 0) return SSA_OK;
   if (!codes || !scales || !x) return SSA_ERR_INVALID_ARG;
-  if ((reinterpret_cast<uintptr_t>(x) & 15u) || (reinterpret_cast<uintptr_t>(codes) & 7u) ||
+  if (((reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(codes)) & 15u) ||
       (reinterpret_cast<uintptr_t>(scales) & 3u))
     return SSA_ERR_UNSUPPORTED;
   return internal::device_pointers({codes, scales, x});
@@ -143,12 +178,14 @@ int check(const void* codes, const float* scales, const void* x, int tokens, int
 int launch_restore(const Restore& p, int tensors, int dim, cudaStream_t stream) {
   int heads = 0;
   for (int i = 0; i < tensors; ++i) heads = p.heads[i] > heads ? p.heads[i] : heads;
-  const int64_t want = (static_cast<int64_t>(p.tokens) * heads * (dim / 8) + kThreads - 1) / kThreads;
-  const unsigned blocks = static_cast<unsigned>(want < 148 * 32 ? want : 148 * 32);
+  const int rows = p.tokens < kT ? p.tokens : kT;
+  const int64_t pieces = static_cast<int64_t>(rows) * heads * (dim / 8);
+  const dim3 grid(static_cast<unsigned>((static_cast<int64_t>(p.tokens) + kT - 1) / kT),
+                  static_cast<unsigned>((pieces + kThreads * kPieces - 1) / (kThreads * kPieces)), tensors);
   if (dim == 64)
-    restore_kernel<64><<<dim3(blocks, tensors), kThreads, 0, stream>>>(p);
+    restore_kernel<64><<<grid, kThreads, 0, stream>>>(p);
   else
-    restore_kernel<128><<<dim3(blocks, tensors), kThreads, 0, stream>>>(p);
+    restore_kernel<128><<<grid, kThreads, 0, stream>>>(p);
   const cudaError_t e = cudaGetLastError();
   return e == cudaSuccess ? SSA_OK : internal::fail(e);
 }

@@ -284,7 +284,7 @@ int ssa_bwd(const void* dout, const void* q, const void* k, const void* v, const
  * ssa_restore_fp8 returns s * decode(code), exact in bf16.
  *   x       device bf16 [total_tokens, num_heads, head_dim], 16-byte aligned;
  *           head_dim 64 or 128
- *   codes   device bytes of the same shape, 8-byte aligned
+ *   codes   device bytes of the same shape, 16-byte aligned
  *   scales  device float [ceil(total_tokens / 128)][num_heads]
  */
 int ssa_save_fp8(const void* x, void* codes, float* scales, int total_tokens, int num_heads, int head_dim,

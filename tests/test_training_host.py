@@ -87,7 +87,7 @@ def test_saved_refusals(ssa):
     for f in (save, back):
         assert f(T=-1) == INVALID and f(H=0) == INVALID and f(H=65536) == INVALID
         assert f(x=None) == INVALID and f(c=None) == INVALID and f(s=None) == INVALID
-        assert f(D=96) == UNSUPPORTED and f(x=MIS) == UNSUPPORTED and f(c=ctypes.c_void_p(0x10004)) == UNSUPPORTED
+        assert f(D=96) == UNSUPPORTED and f(x=MIS) == UNSUPPORTED and f(c=MIS) == UNSUPPORTED
         assert f(T=0) == OK
         assert f() == INVALID  # not device memory
     need = ssa.bwd_fp8_workspace_bytes(256, 1, 4, 2, 128)
@@ -96,7 +96,7 @@ def test_saved_refusals(ssa):
         size, None)
     for kw in (dict(q=None), dict(qs=None), dict(v=None), dict(H=0), dict(Hk=0), dict(total=-1)):
         assert f8(**kw) == INVALID, kw
-    assert f8(D=32) == UNSUPPORTED and f8(q=ctypes.c_void_p(0x10004)) == UNSUPPORTED
+    assert f8(D=32) == UNSUPPORTED and f8(q=MIS) == UNSUPPORTED
     assert f8(total=0) == OK
 
 

@@ -25,21 +25,21 @@
 // on the order in which CTAs run.
 //
 // Warps 0-7: element-wise work, 64 columns of one of the 128 TMEM lanes per
-// thread; warp 8: TMA producer; warp 9: tcgen05 issuer (one thread).
+// thread; warp 8: TMA producer; warps 9-11: one tcgen05 issuing thread each, for
+// S, for dP and for the accumulating products. With one issuer for all of them
+// its waits (110-300 cycles each while its own MMAs run, four or five per tile)
+// drained the tensor pipe: 3280 and 2976 cycles per tile in the kv and q role.
 // TMEM (512 columns): two score regions X [0,128) and Y [128,256), accA
 // [256,256+D), and
 //   kv role: accB [384,384+D). Tile j has S in one score region and dP in the
 //            other; P and dS, as bf16 pairs, replace S once it is in registers
 //            (P in the first 32 of each 64 columns, dS in the second). S of the
 //            next tile takes the place of dP as soon as that has been read,
-//            and dP of the next tile that of P and dS, behind the products
-//            that read them: the regions change places with every tile.
+//            and dP of the next tile that of P and dS once the products that
+//            read them are complete: the regions change places with every tile.
 //   q role:  S in X, dP in Y, dS in two buffers [384,448) and [448,512), so S
 //            and dP of the next tile are formed as soon as this tile's have
 //            been read.
-// MMAs issued by one thread execute in order, so an MMA that overwrites P or
-// dS cannot pass the one ahead of it that reads them.
-//
 // Every wait is bounded in time; one that runs out records SSA_ERR_TIMEOUT in
 // the status word, the other roles leave at their next wait, in-flight loads
 // and MMAs are drained and TMEM is released.
@@ -62,8 +62,8 @@ using namespace sm100;
 
 constexpr int kT = SSA_TILE;  // rows of every tile
 constexpr int kTmaWarp = 8;
-constexpr int kMmaWarp = 9;
-constexpr int kThreads = 320;
+constexpr int kSWarp = 9, kDPWarp = 10, kAccWarp = 11;  // issuers
+constexpr int kThreads = 32 * (kAccWarp + 1);
 constexpr int kAStages = 3;  // ring A lives from its S to its dS product, longer than ring B
 constexpr int kBStages = 2;
 constexpr uint32_t kTmemCols = 512;
@@ -93,16 +93,14 @@ struct Unit {
 struct Ctl {
   uint64_t fix_full;
   uint64_t a_full[kAStages], a_empty[kAStages];
-  uint64_t b_full[kBStages], b_empty[kBStages];
-  uint64_t s_full, dp_full;           // MMA results ready
-  // Element-wise warps. q role: S is in registers, dP is in registers; kv role
-  // (s_done): P is stored and dP in registers.
-  uint64_t s_done, dp_done;
-  // dS of even and odd tiles is stored. Two, because in the q role S and dP of tile j + 1
-  // are issued before the issuer waits for dS(j): the element-wise warps may
-  // finish both before it looks, and one barrier would have gone round.
-  uint64_t ds_full[2];
-  uint64_t acc_full, drain;
+  uint64_t b_full[kBStages], b_empty[kBStages];  // b_empty: q role (kv role: a_empty says it)
+  uint64_t s_full, dp_full;  // MMA results ready
+  // Element-wise warps: S in registers (q role), dP in registers, and, for even
+  // and odd tiles, P (kv role) and dS stored. Those two have two barriers: the
+  // element-wise warps may be a tile ahead of the accumulating issuer, and a
+  // single barrier would have gone round before it looked.
+  uint64_t s_done, dp_done, p_full[2], ds_full[2];
+  uint64_t acc_full, drain[3];
   uint32_t tmem_base;
   int abort_flag;
   int info[kAStages];  // rows of the ring tile inside the sequence (128 but for the last), or -1: no more tiles
@@ -296,8 +294,16 @@ __device__ __forceinline__ void run_role(const CUtensorMap* tmFixA, const CUtens
   auto b_empty = [&](int i) { return smem_u32(&ctl.b_empty[i]); };
   const uint32_t s_full = smem_u32(&ctl.s_full), dp_full = smem_u32(&ctl.dp_full);
   const uint32_t s_done = smem_u32(&ctl.s_done), dp_done = smem_u32(&ctl.dp_done);
+  auto p_full = [&](int j) { return smem_u32(&ctl.p_full[j & 1]); };    // phase j >> 1
   auto ds_full = [&](int j) { return smem_u32(&ctl.ds_full[j & 1]); };  // phase j >> 1
   const uint32_t fix_full = smem_u32(&ctl.fix_full), acc_full = smem_u32(&ctl.acc_full);
+  // Tile j's ring A stage is free, which also says that the products that read
+  // its P and dS, and (kv role) its ring B stage and row values, are complete.
+  auto acc_done = [&](int j) { return smem_u32(&ctl.a_empty[j % kAStages]); };  // phase j / kAStages
+  // kv role: the score region of S (then P and dS) of tile j; dP of tile j is in
+  // the other one. q role: S always in X, dP in Y.
+  auto col_s = [&](int j) { return (Q || !(j & 1)) ? kColS : kColDP; };
+  auto col_dp = [&](int j) { return (Q || !(j & 1)) ? kColDP : kColS; };
 
   if (warp == kTmaWarp) {
     // ------------------------------------------------------------ producer
@@ -347,12 +353,11 @@ __device__ __forceinline__ void run_role(const CUtensorMap* tmFixA, const CUtens
             tma_load_3d(smem_u32(smem + L::kRingA + sa * L::kTileBytes + ch * L::kChunkBytes), tmRingA, a_full(sa),
                         ch * 64, ring_head, u.start + t * kT);
           const int n = it++;
-          if (n >= kBStages && !(ok = wait_bar(b_empty(sb), ((n / kBStages) - 1) & 1, abort_flag, p.status))) break;
-          if (!Q) {
-            // The row values share ring B's barrier, but are read until dS of
-            // their tile: their slot is free with tile n - 2's ring A stage.
-            const int old = n - kBStages;
-            if (old >= 0 && !(ok = wait_bar(a_empty(old % kAStages), (old / kAStages) & 1, abort_flag, p.status))) break;
+          if (n >= kBStages) {
+            const int old = n - kBStages;  // the tile that had this ring B stage (kv role: and row values)
+            if (!(ok = Q ? wait_bar(b_empty(sb), (old / kBStages) & 1, abort_flag, p.status)
+                         : wait_bar(acc_done(old), (old / kAStages) & 1, abort_flag, p.status)))
+              break;
           }
           mbar_arrive_expect_tx(b_full(sb), L::kTileBytes + (Q ? 0 : L::kRowBytes));
           if (!Q)
@@ -384,8 +389,8 @@ __device__ __forceinline__ void run_role(const CUtensorMap* tmFixA, const CUtens
           if (b_issued > i) drain_wait(b_full(i), ((b_issued - 1 - i) / kBStages) & 1, p.status);
       }
     }
-  } else if (warp == kMmaWarp) {
-    // ------------------------------------------------------- tcgen05 issuer
+  } else if (warp >= kSWarp) {
+    // ------------------------------------------------------ tcgen05 issuers
     if (lane == 0) {
       constexpr uint32_t idesc_s = idesc_bf16_f32(kT, kT, false);
       constexpr uint32_t idesc_acc = idesc_bf16_f32(kT, D, true);
@@ -417,73 +422,53 @@ __device__ __forceinline__ void run_role(const CUtensorMap* tmFixA, const CUtens
       auto ring_a = [&](int j) { return L::kRingA + (j % kAStages) * L::kTileBytes; };
       auto ring_b = [&](int j) { return L::kRingB + (j % kBStages) * L::kTileBytes; };
       // True when tile j exists; its A tile has landed then.
-      auto has = [&](int j, bool& ok) {
+      bool ok = true;
+      auto has = [&](int j) {
         ok = wait(a_full(j % kAStages), (j / kAStages) & 1);
         return ok && *static_cast<volatile int*>(&ctl.info[j % kAStages]) >= 0;
       };
-      bool ok = wait(fix_full, 0);
-      bool more = ok && has(0, ok);
-      if (more) {
-        tc_fence_after();
-        product(kColS, L::kFixA, ring_a(0));
-        tc_commit(s_full);
-        if ((ok = wait(b_full(0), 0))) {
+      if (warp == kSWarp) {
+        // S(j), once S(j-1) (q role) or dP(j-1) (kv role), which it overwrites, has been read.
+        ok = wait(fix_full, 0);
+        for (int j = 0; ok && has(j); ++j) {
+          if (j > 0 && !(ok = wait(Q ? s_done : dp_done, (j - 1) & 1))) break;
           tc_fence_after();
-          product(kColDP, L::kFixB, ring_b(0));
+          product(col_s(j), L::kFixA, ring_a(j));
+          tc_commit(s_full);
+        }
+      } else if (warp == kDPWarp) {
+        // dP(j), once dP(j-1) has been read (q role), or P and dS of tile j-1 (kv role) used.
+        ok = wait(fix_full, 0);
+        for (int j = 0; ok && has(j); ++j) {
+          if (!(ok = wait(b_full(j % kBStages), (j / kBStages) & 1))) break;
+          if (j > 0 && !(ok = Q ? wait(dp_done, (j - 1) & 1) : wait(acc_done(j - 1), ((j - 1) / kAStages) & 1))) break;
+          tc_fence_after();
+          product(col_dp(j), L::kFixB, ring_b(j));
           tc_commit(dp_full);
-          if (Q) tc_commit(b_empty(0));
+          if (Q) tc_commit(b_empty(j % kBStages));
         }
-      }
-      for (int j = 0; ok && more; ++j) {
-        more = has(j + 1, ok);
-        if (!ok) break;
-        if (Q) {
-          // S(j+1) once S(j) is in registers, dP(j+1) once dP(j) is, then dQ += dS(j) K_j.
-          if (more) {
-            if (!(ok = wait(s_done, j & 1))) break;
-            tc_fence_after();
-            product(kColS, L::kFixA, ring_a(j + 1));
-            tc_commit(s_full);
-            if (!(ok = wait(b_full((j + 1) % kBStages), ((j + 1) / kBStages) & 1))) break;
-            if (!(ok = wait(dp_done, j & 1))) break;
-            tc_fence_after();
-            product(kColDP, L::kFixB, ring_b(j + 1));
-            tc_commit(dp_full);
-            tc_commit(b_empty((j + 1) % kBStages));
-          }
-          if (!(ok = wait(ds_full(j), (j >> 1) & 1))) break;
-          tc_fence_after();
-          accumulate(kColAccA, kColDS + (j & 1) * 64, 0, ring_a(j), j > 0);
-          tc_commit(a_empty(j % kAStages));
-        } else {
-          // Once P(j) is stored and dP(j) in registers: S(j+1) over dP(j), for the
-          // element-wise warps to go on with, and dV += P(j)^T dO_j; once dS(j)
-          // is stored: dK += dS(j)^T Q_j and, over P(j) and dS(j), dP(j+1).
-          const uint32_t here = (j & 1) ? kColDP : kColS, there = (j & 1) ? kColS : kColDP;
-          if (!(ok = wait(s_done, j & 1))) break;
-          tc_fence_after();
-          if (more) {
-            product(there, L::kFixA, ring_a(j + 1));
-            tc_commit(s_full);
-          }
-          accumulate(kColAccB, here, 32, ring_b(j), j > 0);
-          tc_commit(b_empty(j % kBStages));
-          if (more && !(ok = wait(b_full((j + 1) % kBStages), ((j + 1) / kBStages) & 1))) break;
-          if (!(ok = wait(ds_full(j), (j >> 1) & 1))) break;
-          tc_fence_after();
-          accumulate(kColAccA, here + 32, 32, ring_a(j), j > 0);
-          tc_commit(a_empty(j % kAStages));
-          if (more) {
-            product(here, L::kFixB, ring_b(j + 1));
-            tc_commit(dp_full);
-          }
-        }
-      }
-      if (ok) {
-        tc_commit(acc_full);
       } else {
-        tc_commit(smem_u32(&ctl.drain));
-        drain_wait(smem_u32(&ctl.drain), 0, p.status);
+        // q role: dQ += dS(j) K_j. kv role: dV += P(j)^T dO_j, dK += dS(j)^T Q_j.
+        for (int j = 0; ok && has(j); ++j) {
+          if (!Q) {
+            if (!(ok = wait(p_full(j), (j >> 1) & 1))) break;
+            tc_fence_after();
+            accumulate(kColAccB, col_s(j), 32, ring_b(j), j > 0);
+          }
+          if (!(ok = wait(ds_full(j), (j >> 1) & 1))) break;
+          tc_fence_after();
+          if (Q)
+            accumulate(kColAccA, kColDS + (j & 1) * 64, 0, ring_a(j), j > 0);
+          else
+            accumulate(kColAccA, col_s(j) + 32, 32, ring_a(j), j > 0);
+          tc_commit(acc_done(j));
+        }
+        if (ok) tc_commit(acc_full);
+      }
+      if (!ok) {  // let every MMA issued so far finish before TMEM is released
+        const uint32_t drain = smem_u32(&ctl.drain[warp - kSWarp]);
+        tc_commit(drain);
+        drain_wait(drain, 0, p.status);
       }
     }
   } else {
@@ -510,11 +495,8 @@ __device__ __forceinline__ void run_role(const CUtensorMap* tmFixA, const CUtens
       if (!Q && !(ok = warp_wait(b_full(j % kBStages), (j / kBStages) & 1, abort_flag, p.status))) break;
       if (!(ok = warp_wait(s_full, j & 1, abort_flag, p.status))) break;
       tc_fence_after();
-      // kv role: the two score regions change places with every tile.
-      const uint32_t col_s = lanes + ((Q || !(j & 1)) ? kColS : kColDP) + half * 64;
-      const uint32_t col_dp = lanes + ((Q || !(j & 1)) ? kColDP : kColS) + half * 64;
       uint32_t s[64];
-      tmem_ld_x64_async(col_s, s);
+      tmem_ld_x64_async(lanes + col_s(j) + half * 64, s);
       if (valid < kT) {
         // The tile ends past the sequence. Its rows out there are summation
         // rows of the accumulating products: they must be zeros, not whatever
@@ -552,14 +534,15 @@ __device__ __forceinline__ void run_role(const CUtensorMap* tmFixA, const CUtens
       if (!Q) {
 #pragma unroll
         for (int i = 0; i < 32; ++i) pk[i] = pack_bf16x2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1]));
-        tmem_st_x32(col_s, pk);
+        tmem_st_x32(lanes + col_s(j) + half * 64, pk);
+        warp_arrive(p_full(j), lane);
       }
       if (!(ok = warp_wait(dp_full, j & 1, abort_flag, p.status))) break;
       tc_fence_after();
       uint32_t d[64];
-      tmem_ld_x64_async(col_dp, d);
+      tmem_ld_x64_async(lanes + col_dp(j) + half * 64, d);
       tmem_wait_ld_tied(d);
-      warp_arrive(Q ? dp_done : s_done, lane);
+      warp_arrive(dp_done, lane);
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
         const float4 n4 = Q ? make_float4(row_ndelta, row_ndelta, row_ndelta, row_ndelta)
@@ -580,7 +563,11 @@ __device__ __forceinline__ void run_role(const CUtensorMap* tmFixA, const CUtens
           pk[i] = c >= valid ? 0u : (c + 1 >= valid ? pk[i] & 0xFFFFu : pk[i]);
         }
       }
-      tmem_st_x32(Q ? lanes + kColDS + (j & 1) * 64 + half * 32 : col_s + 32, pk);
+      if (Q) {  // the buffer's last reader was dQ += dS(j-2) K
+        if (j >= 2 && !(ok = warp_wait(acc_done(j - 2), ((j - 2) / kAStages) & 1, abort_flag, p.status))) break;
+        tc_fence_after();
+      }
+      tmem_st_x32(lanes + (Q ? kColDS + (j & 1) * 64 + half * 32 : col_s(j) + half * 64 + 32), pk);
       warp_arrive(ds_full(j), lane);
     }
 
@@ -646,14 +633,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(smem_u32(&ctl.dp_full), 1);
     mbar_init(smem_u32(&ctl.s_done), 8);
     mbar_init(smem_u32(&ctl.dp_done), 8);
-    mbar_init(smem_u32(&ctl.ds_full[0]), 8);
-    mbar_init(smem_u32(&ctl.ds_full[1]), 8);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_u32(&ctl.p_full[i]), 8);
+      mbar_init(smem_u32(&ctl.ds_full[i]), 8);
+    }
     mbar_init(smem_u32(&ctl.acc_full), 1);
-    mbar_init(smem_u32(&ctl.drain), 1);
+    for (int i = 0; i < 3; ++i) mbar_init(smem_u32(&ctl.drain[i]), 1);
     ctl.abort_flag = 0;
     fence_mbar_init();
   }
-  if (warp == kMmaWarp) {
+  if (warp == kSWarp) {
     tmem_alloc(smem_u32(&ctl.tmem_base), kTmemCols);
     tmem_relinquish();
   }
@@ -669,7 +658,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncwarp();
   tc_fence_before();
   __syncthreads();
-  if (warp == kMmaWarp) {
+  if (warp == kSWarp) {
     tc_fence_after();
     tmem_dealloc(ctl.tmem_base, kTmemCols);
   }

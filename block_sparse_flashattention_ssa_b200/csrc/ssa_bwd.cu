@@ -24,9 +24,9 @@
 // one owner: no atomics, no fp32 dQ in memory, and results that do not depend
 // on the order in which CTAs run.
 //
-// Warps 0-7: element-wise work, 64 columns of one of the 128 TMEM lanes per
-// thread; warp 8: TMA producer; warps 9-11: one tcgen05 issuing thread each, for
-// S, for dP and for the accumulating products. With one issuer for all of them
+// Warp 0: TMA producer; warps 1-3: one tcgen05 issuing thread each, for S, for
+// dP and for the accumulating products; warps 4-11: element-wise work, 64
+// columns of one of the 128 TMEM lanes per thread. With one issuer for all of them
 // its waits (110-300 cycles each while its own MMAs run, four or five per tile)
 // drained the tensor pipe: 3280 and 2976 cycles per tile in the kv and q role.
 // TMEM (512 columns): two score regions X [0,128) and Y [128,256), accA
@@ -37,9 +37,9 @@
 //            next tile takes the place of dP as soon as that has been read,
 //            and dP of the next tile that of P and dS once the products that
 //            read them are complete: the regions change places with every tile.
-//   q role:  S in X, dP in Y, dS in two buffers [384,448) and [448,512), so S
-//            and dP of the next tile are formed as soon as this tile's have
-//            been read.
+//   q role:  S in X and Z [384,512) by turns, dP in Y; dS replaces S. S of a
+//            tile is formed as soon as dQ has taken dS of the tile before last,
+//            dP as soon as the last tile's has been read.
 // Every wait is bounded in time; one that runs out records SSA_ERR_TIMEOUT in
 // the status word, the other roles leave at their next wait, in-flight loads
 // and MMAs are drained and TMEM is released.
@@ -61,13 +61,18 @@ namespace {
 using namespace sm100;
 
 constexpr int kT = SSA_TILE;  // rows of every tile
-constexpr int kTmaWarp = 8;
-constexpr int kSWarp = 9, kDPWarp = 10, kAccWarp = 11;  // issuers
-constexpr int kThreads = 32 * (kAccWarp + 1);
+// The issuers come first: a warp scheduler prefers the older of its warps, and
+// an issuer behind two element-wise warps in their arithmetic woke 300-500
+// cycles late.
+constexpr int kTmaWarp = 0;
+constexpr int kSWarp = 1, kDPWarp = 2, kAccWarp = 3;  // issuers
+constexpr int kEwWarp = 4;                            // first of eight element-wise warps
+constexpr int kEwThreads = 256;
+constexpr int kThreads = 32 * kEwWarp + kEwThreads;
 constexpr int kAStages = 3;  // ring A lives from its S to its dS product, longer than ring B
 constexpr int kBStages = 2;
 constexpr uint32_t kTmemCols = 512;
-constexpr uint32_t kColS = 0, kColDP = 128, kColAccA = 256, kColAccB = 384, kColDS = 384;
+constexpr uint32_t kColX = 0, kColY = 128, kColAccA = 256, kColAccB = 384, kColZ = 384;
 constexpr uint32_t kFull = 0xFFFFFFFFu;
 constexpr float kLog2e = 1.44269504088896340736f;
 
@@ -94,12 +99,12 @@ struct Ctl {
   uint64_t fix_full;
   uint64_t a_full[kAStages], a_empty[kAStages];
   uint64_t b_full[kBStages], b_empty[kBStages];  // b_empty: q role (kv role: a_empty says it)
-  uint64_t s_full, dp_full;  // MMA results ready
-  // Element-wise warps: S in registers (q role), dP in registers, and, for even
-  // and odd tiles, P (kv role) and dS stored. Those two have two barriers: the
-  // element-wise warps may be a tile ahead of the accumulating issuer, and a
-  // single barrier would have gone round before it looked.
-  uint64_t s_done, dp_done, p_full[2], ds_full[2];
+  // MMA results ready: S of even and odd tiles, dP; element-wise warps: dP in
+  // registers; P (kv role) and dS of even and odd tiles stored. Two barriers
+  // where the side that completes them may be a tile ahead of the side that
+  // looks (the S issuer of the element-wise warps in the q role, these of the
+  // accumulating issuer): a single one would have gone round.
+  uint64_t s_full[2], dp_full, dp_done, p_full[2], ds_full[2];
   uint64_t acc_full, drain[3];
   uint32_t tmem_base;
   int abort_flag;
@@ -152,6 +157,14 @@ __device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t parity, int* s
 
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag, int* status) {
   return __all_sync(kFull, wait_bar(bar, parity, abort_flag, status));
+}
+
+// warp_wait for a barrier that was looked at before (`seen`, per lane): a wait
+// that is already over costs a warp 110 cycles, nearly all of it latency that a
+// look some work ahead hides.
+__device__ __forceinline__ bool warp_wait_seen(bool seen, uint32_t bar, uint32_t parity, volatile int* abort_flag,
+                                               int* status) {
+  return __all_sync(kFull, seen) || warp_wait(bar, parity, abort_flag, status);
 }
 
 __device__ __forceinline__ void warp_arrive(uint32_t bar, int lane) {
@@ -292,18 +305,17 @@ __device__ __forceinline__ void run_role(const CUtensorMap* tmFixA, const CUtens
   auto a_empty = [&](int i) { return smem_u32(&ctl.a_empty[i]); };
   auto b_full = [&](int i) { return smem_u32(&ctl.b_full[i]); };
   auto b_empty = [&](int i) { return smem_u32(&ctl.b_empty[i]); };
-  const uint32_t s_full = smem_u32(&ctl.s_full), dp_full = smem_u32(&ctl.dp_full);
-  const uint32_t s_done = smem_u32(&ctl.s_done), dp_done = smem_u32(&ctl.dp_done);
+  const uint32_t dp_full = smem_u32(&ctl.dp_full), dp_done = smem_u32(&ctl.dp_done);
+  auto s_full = [&](int j) { return smem_u32(&ctl.s_full[j & 1]); };    // phase j >> 1
   auto p_full = [&](int j) { return smem_u32(&ctl.p_full[j & 1]); };    // phase j >> 1
   auto ds_full = [&](int j) { return smem_u32(&ctl.ds_full[j & 1]); };  // phase j >> 1
   const uint32_t fix_full = smem_u32(&ctl.fix_full), acc_full = smem_u32(&ctl.acc_full);
   // Tile j's ring A stage is free, which also says that the products that read
   // its P and dS, and (kv role) its ring B stage and row values, are complete.
   auto acc_done = [&](int j) { return smem_u32(&ctl.a_empty[j % kAStages]); };  // phase j / kAStages
-  // kv role: the score region of S (then P and dS) of tile j; dP of tile j is in
-  // the other one. q role: S always in X, dP in Y.
-  auto col_s = [&](int j) { return (Q || !(j & 1)) ? kColS : kColDP; };
-  auto col_dp = [&](int j) { return (Q || !(j & 1)) ? kColDP : kColS; };
+  // The region of S of tile j, then of its dS and (kv role) P; and that of dP.
+  auto col_s = [&](int j) { return j & 1 ? (Q ? kColZ : kColY) : kColX; };
+  auto col_dp = [&](int j) { return Q || !(j & 1) ? kColY : kColX; };
 
   if (warp == kTmaWarp) {
     // ------------------------------------------------------------ producer
@@ -389,7 +401,7 @@ __device__ __forceinline__ void run_role(const CUtensorMap* tmFixA, const CUtens
           if (b_issued > i) drain_wait(b_full(i), ((b_issued - 1 - i) / kBStages) & 1, p.status);
       }
     }
-  } else if (warp >= kSWarp) {
+  } else if (warp < kEwWarp) {
     // ------------------------------------------------------ tcgen05 issuers
     if (lane == 0) {
       constexpr uint32_t idesc_s = idesc_bf16_f32(kT, kT, false);
@@ -407,15 +419,15 @@ __device__ __forceinline__ void run_role(const CUtensorMap* tmFixA, const CUtens
         }
       };
       // acc += E ring with E (bf16 pairs, 128 x 128) in TMEM and the ring tile
-      // MN-major (d contiguous), 16 of its rows per MMA; `gap` columns lie
-      // between the two halves of E.
-      auto accumulate = [&](uint32_t acc, uint32_t e, uint32_t gap, int ring, bool more) {
+      // MN-major (d contiguous), 16 of its rows per MMA; the two halves of E
+      // are 64 columns apart.
+      auto accumulate = [&](uint32_t acc, uint32_t e, int ring, bool more) {
         const uint64_t db = smem_desc_sw128(smem_u32(smem + ring), L::kChunkBytes, 1024);
         const uint32_t b_lo = static_cast<uint32_t>(db);
         const uint64_t b_hi = db & 0xFFFFFFFF00000000ull;
 #pragma unroll
         for (int ks = 0; ks < kT / 16; ++ks)
-          mma_ts(tmem + acc, tmem + e + ks * 8 + (ks >= 4 ? gap : 0), b_hi | (b_lo + (ks * 16 * 128 >> 4)), idesc_acc,
+          mma_ts(tmem + acc, tmem + e + ks * 8 + (ks >= 4 ? 32 : 0), b_hi | (b_lo + (ks * 16 * 128 >> 4)), idesc_acc,
                  (more || ks > 0) ? 1u : 0u);
       };
       auto wait = [&](uint32_t bar, int parity) { return wait_bar(bar, parity, abort_flag, p.status); };
@@ -428,13 +440,15 @@ __device__ __forceinline__ void run_role(const CUtensorMap* tmFixA, const CUtens
         return ok && *static_cast<volatile int*>(&ctl.info[j % kAStages]) >= 0;
       };
       if (warp == kSWarp) {
-        // S(j), once S(j-1) (q role) or dP(j-1) (kv role), which it overwrites, has been read.
+        // S(j), once dS(j-2) is used (q role) or dP(j-1) has been read (kv role).
         ok = wait(fix_full, 0);
         for (int j = 0; ok && has(j); ++j) {
-          if (j > 0 && !(ok = wait(Q ? s_done : dp_done, (j - 1) & 1))) break;
+          if (Q ? j > 1 && !(ok = wait(acc_done(j - 2), ((j - 2) / kAStages) & 1))
+                : j > 0 && !(ok = wait(dp_done, (j - 1) & 1)))
+            break;
           tc_fence_after();
           product(col_s(j), L::kFixA, ring_a(j));
-          tc_commit(s_full);
+          tc_commit(s_full(j));
         }
       } else if (warp == kDPWarp) {
         // dP(j), once dP(j-1) has been read (q role), or P and dS of tile j-1 (kv role) used.
@@ -447,20 +461,17 @@ __device__ __forceinline__ void run_role(const CUtensorMap* tmFixA, const CUtens
           tc_commit(dp_full);
           if (Q) tc_commit(b_empty(j % kBStages));
         }
-      } else {
+      } else {  // kAccWarp
         // q role: dQ += dS(j) K_j. kv role: dV += P(j)^T dO_j, dK += dS(j)^T Q_j.
         for (int j = 0; ok && has(j); ++j) {
           if (!Q) {
             if (!(ok = wait(p_full(j), (j >> 1) & 1))) break;
             tc_fence_after();
-            accumulate(kColAccB, col_s(j), 32, ring_b(j), j > 0);
+            accumulate(kColAccB, col_s(j), ring_b(j), j > 0);
           }
           if (!(ok = wait(ds_full(j), (j >> 1) & 1))) break;
           tc_fence_after();
-          if (Q)
-            accumulate(kColAccA, kColDS + (j & 1) * 64, 0, ring_a(j), j > 0);
-          else
-            accumulate(kColAccA, col_s(j) + 32, 32, ring_a(j), j > 0);
+          accumulate(kColAccA, col_s(j) + (Q ? 0 : 32), ring_a(j), j > 0);
           tc_commit(acc_done(j));
         }
         if (ok) tc_commit(acc_full);
@@ -473,7 +484,7 @@ __device__ __forceinline__ void run_role(const CUtensorMap* tmFixA, const CUtens
     }
   } else {
     // -------------------------------------------------------- element-wise
-    const int half = warp >> 2;  // columns [64 half, 64 half + 64)
+    const int half = (warp - kEwWarp) >> 2;  // columns [64 half, 64 half + 64)
     const int row = (warp & 3) * 32 + lane;
     const uint32_t lanes = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
     const bool row_valid = u.block * kT + row < u.S;
@@ -484,25 +495,28 @@ __device__ __forceinline__ void run_role(const CUtensorMap* tmFixA, const CUtens
       row_ndelta = r[kT + row];
     }
     const float2 c2 = make_float2(p.c2, p.c2);
-    bool ok = true;
-    int j = 0;
-    for (;; ++j) {
-      const int sa = j % kAStages;
-      if (!(ok = warp_wait(a_full(sa), (j / kAStages) & 1, abort_flag, p.status))) break;
-      const int valid = *static_cast<volatile int*>(&ctl.info[sa]);
-      if (valid < 0) break;
+    // Waits are looked at ahead of their time, over work that does not need
+    // them. The check right behind the arrival on dp_done also keeps the
+    // compiler from moving that arrival behind the arithmetic that follows it.
+    bool ok = warp_wait(a_full(0), 0, abort_flag, p.status);
+    int j = 0, valid = ok ? *static_cast<volatile int*>(&ctl.info[0]) : -1;
+    bool s_seen = false, rows_seen = false;
+    int sa = 0, a_phase = 0;  // j % kAStages, (j / kAStages) & 1
+    for (; ok && valid >= 0; ++j) {
+      const int sa_next = sa + 1 == kAStages ? 0 : sa + 1, a_phase_next = a_phase ^ (sa_next == 0 ? 1 : 0);
       const float* rows = reinterpret_cast<const float*>(smem + L::kRows + (j % kBStages) * L::kRowBytes) + half * 64;
-      if (!Q && !(ok = warp_wait(b_full(j % kBStages), (j / kBStages) & 1, abort_flag, p.status))) break;
-      if (!(ok = warp_wait(s_full, j & 1, abort_flag, p.status))) break;
+      if (!Q && !(ok = warp_wait_seen(rows_seen, b_full(j % kBStages), (j / kBStages) & 1, abort_flag, p.status))) break;
+      if (!(ok = warp_wait_seen(s_seen, s_full(j), (j >> 1) & 1, abort_flag, p.status))) break;
       tc_fence_after();
       uint32_t s[64];
       tmem_ld_x64_async(lanes + col_s(j) + half * 64, s);
+      const bool a_seen = mbar_test_wait(a_full(sa_next), a_phase_next);
       if (valid < kT) {
         // The tile ends past the sequence. Its rows out there are summation
         // rows of the accumulating products: they must be zeros, not whatever
         // memory holds (NaN times a zero probability is NaN).
         const int words = (kT - valid) * 8;  // 16-byte words of a chunk's rows past the end
-        for (int i = threadIdx.x; i < L::kChunks * words; i += 256) {
+        for (int i = threadIdx.x - 32 * kEwWarp; i < L::kChunks * words; i += kEwThreads) {
           const int at = (i / words) * L::kChunkBytes + valid * 128 + (i % words) * 16;
           *reinterpret_cast<uint4*>(smem + L::kRingA + sa * L::kTileBytes + at) = make_uint4(0, 0, 0, 0);
           if (!Q)
@@ -511,8 +525,14 @@ __device__ __forceinline__ void run_role(const CUtensorMap* tmFixA, const CUtens
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       }
       tmem_wait_ld_tied(s);
-      if (Q) warp_arrive(s_done, lane);
+      if (valid < kT) {  // no probability past the end, whatever stands there
+#pragma unroll
+        for (int i = 0; i < 64; ++i)
+          if (half * 64 + i >= valid) s[i] = __float_as_uint(-INFINITY);
+      }
+      const bool dp_seen = mbar_test_wait(dp_full, j & 1);
       // P = 2^(c2 S - L log2 e)
+      uint32_t pk[32];
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
         const float4 b4 = Q ? make_float4(row_bias, row_bias, row_bias, row_bias) : reinterpret_cast<const float4*>(rows)[i];
@@ -520,29 +540,38 @@ __device__ __forceinline__ void run_role(const CUtensorMap* tmFixA, const CUtens
                                 make_float2(b4.x, b4.y));
         const float2 e1 = ffma2(make_float2(__uint_as_float(s[4 * i + 2]), __uint_as_float(s[4 * i + 3])), c2,
                                 make_float2(b4.z, b4.w));
-        s[4 * i] = __float_as_uint(ex2_approx(e0.x));
-        s[4 * i + 1] = __float_as_uint(ex2_approx(e0.y));
-        s[4 * i + 2] = __float_as_uint(ex2_approx(e1.x));
-        s[4 * i + 3] = __float_as_uint(ex2_approx(e1.y));
+        const float2 p0 = make_float2(ex2_approx(e0.x), ex2_approx(e0.y));
+        const float2 p1 = make_float2(ex2_approx(e1.x), ex2_approx(e1.y));
+        s[4 * i] = __float_as_uint(p0.x);
+        s[4 * i + 1] = __float_as_uint(p0.y);
+        s[4 * i + 2] = __float_as_uint(p1.x);
+        s[4 * i + 3] = __float_as_uint(p1.y);
+        if (!Q) {
+          pk[2 * i] = pack_bf16x2(p0.x, p0.y);
+          pk[2 * i + 1] = pack_bf16x2(p1.x, p1.y);
+        }
       }
-      if (valid < kT) {  // also where the score of a row past the end was not finite
-#pragma unroll
-        for (int i = 0; i < 64; ++i)
-          if (half * 64 + i >= valid) s[i] = 0u;
-      }
-      uint32_t pk[32];
       if (!Q) {
-#pragma unroll
-        for (int i = 0; i < 32; ++i) pk[i] = pack_bf16x2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1]));
         tmem_st_x32(lanes + col_s(j) + half * 64, pk);
         warp_arrive(p_full(j), lane);
       }
-      if (!(ok = warp_wait(dp_full, j & 1, abort_flag, p.status))) break;
+      if (!(ok = warp_wait_seen(dp_seen, dp_full, j & 1, abort_flag, p.status))) break;
       tc_fence_after();
       uint32_t d[64];
       tmem_ld_x64_async(lanes + col_dp(j) + half * 64, d);
       tmem_wait_ld_tied(d);
       warp_arrive(dp_done, lane);
+      if (!(ok = warp_wait_seen(a_seen, a_full(sa_next), a_phase_next, abort_flag, p.status))) break;
+      const int valid_next = *static_cast<volatile int*>(&ctl.info[sa_next]);
+      if (Q)
+        s_seen = mbar_test_wait(s_full(j + 1), ((j + 1) >> 1) & 1);
+      else
+        rows_seen = mbar_test_wait(b_full((j + 1) % kBStages), ((j + 1) / kBStages) & 1);
+      if (valid < kT) {
+#pragma unroll
+        for (int i = 0; i < 64; ++i)
+          if (half * 64 + i >= valid) d[i] = 0u;
+      }
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
         const float4 n4 = Q ? make_float4(row_ndelta, row_ndelta, row_ndelta, row_ndelta)
@@ -556,19 +585,11 @@ __device__ __forceinline__ void run_role(const CUtensorMap* tmFixA, const CUtens
         pk[2 * i] = pack_bf16x2(x.x, x.y);
         pk[2 * i + 1] = pack_bf16x2(y.x, y.y);
       }
-      if (valid < kT) {  // dP past the end may not be finite
-#pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          const int c = half * 64 + 2 * i;
-          pk[i] = c >= valid ? 0u : (c + 1 >= valid ? pk[i] & 0xFFFFu : pk[i]);
-        }
-      }
-      if (Q) {  // the buffer's last reader was dQ += dS(j-2) K
-        if (j >= 2 && !(ok = warp_wait(acc_done(j - 2), ((j - 2) / kAStages) & 1, abort_flag, p.status))) break;
-        tc_fence_after();
-      }
-      tmem_st_x32(lanes + (Q ? kColDS + (j & 1) * 64 + half * 32 : col_s(j) + half * 64 + 32), pk);
+      tmem_st_x32(lanes + col_s(j) + half * 64 + (Q ? 0 : 32), pk);
       warp_arrive(ds_full(j), lane);
+      valid = valid_next;
+      sa = sa_next;
+      a_phase = a_phase_next;
     }
 
     // Epilogue: this thread's row and half of the D columns of each accumulator.
@@ -629,11 +650,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(smem_u32(&ctl.b_full[i]), 1);
       mbar_init(smem_u32(&ctl.b_empty[i]), 1);
     }
-    mbar_init(smem_u32(&ctl.s_full), 1);
     mbar_init(smem_u32(&ctl.dp_full), 1);
-    mbar_init(smem_u32(&ctl.s_done), 8);
     mbar_init(smem_u32(&ctl.dp_done), 8);
     for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_u32(&ctl.s_full[i]), 1);
       mbar_init(smem_u32(&ctl.p_full[i]), 8);
       mbar_init(smem_u32(&ctl.ds_full[i]), 8);
     }

@@ -31,6 +31,7 @@ functions):
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import numpy as np
@@ -610,6 +611,11 @@ def restore_fp8(codes, scales, out=None, stream=None):
     return _run(dev, stream, (codes, scales, out), body)[0]
 
 
+@functools.lru_cache(maxsize=None)
+def _sections_type(axes):
+    return ctypes.c_int32 * axes
+
+
 def _rows(t, name, dev, total, dim):
     """Check a rotary operand [total, H, dim] whose tokens may lie apart (a
     slice of a fused projection, say); returns its token stride."""
@@ -696,7 +702,7 @@ def rotary(q, k, positions, inv_freq, sections=None, interleaved: bool = False, 
                 raise ValueError(f"{name} overlaps {other}")
     if len(written) == 2 and _rows_overlap(written[0][0], written[0][1], written[1][0], written[1][1]):
         raise ValueError("out_q overlaps out_k")
-    n_pairs = (ctypes.c_int32 * axes)(*counts)
+    n_pairs = _sections_type(axes)(*counts)
 
     def body(handle):
         oq = torch.empty_like(q, memory_format=torch.contiguous_format) if out_q is None else out_q

@@ -17,6 +17,9 @@
 //            S^T = K Q^T, dP^T = V dO^T, dV += P^T dO, dK += dS^T Q;
 //   q role:  128 query rows against the KV tiles they kept;
 //            S = Q K^T, dP = dO V^T, dQ += dS K.
+// When there are too few rows for the SMs, the CTAs of a cluster share one
+// block's tiles between them and add their accumulators up over distributed
+// shared memory, in the order of their ranks.
 // Both roles are one pipeline with the operands exchanged ("fixed" tiles A, B
 // loaded once; "ring" tiles A, B streamed): S = fixA ringA^T, dP = fixB
 // ringB^T, accA += dS ringA, and in the kv role accB += P ringB. S and dP are
@@ -74,6 +77,7 @@ constexpr int kBStages = 2;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColX = 0, kColY = 128, kColAccA = 256, kColAccB = 384, kColZ = 384;
 constexpr uint32_t kFull = 0xFFFFFFFFu;
+constexpr int kSMs = 148;
 constexpr float kLog2e = 1.44269504088896340736f;
 
 struct Params {
@@ -84,9 +88,10 @@ struct Params {
   const float* lse;
   float* rows;  // [num_heads][units][2][128]: -L log2 e, then -D, per query block
   int* status;
-  int batch, total_tokens, num_heads, num_kv_heads, bitmap_words, max_tiles;
+  int batch, total_tokens, max_seqlen, num_heads, num_kv_heads, bitmap_words, max_tiles;
   int units;     // bound on the query blocks of the batch: ceil(total / 128) + batch
   int nq_check;  // query blocks the bitmap was sized for, or -1
+  int split[2];  // CTAs that share a block's tiles: kv role, q role (1, or the cluster's size: a power of two)
   float scale;   // c
   float c2;      // fp32(c log2 e), the forward's score factor
 };
@@ -289,16 +294,37 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
       : "memory");
 }
 
+// All threads of the cluster; orders shared-memory accesses before it against
+// those after it. (Every path to it is bounded in time.)
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release;\n barrier.cluster.wait.acquire;" ::: "memory");
+}
+
+// 16 bytes at this CTA's shared-memory address `addr` in the CTA of rank `rank`.
+__device__ __forceinline__ float4 ld_cluster(uint32_t addr, int rank) {
+  float4 v;
+  asm volatile(
+      "{\n .reg .b32 a;\n mapa.shared::cluster.u32 a, %4, %5;\n ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [a];\n}"
+      : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+      : "r"(addr), "r"(rank)
+      : "memory");
+  return v;
+}
+
 template <int D, bool Q>
 __device__ __forceinline__ void run_role(const CUtensorMap* tmFixA, const CUtensorMap* tmFixB,
                                          const CUtensorMap* tmRingA, const CUtensorMap* tmRingB, const Params& p,
-                                         uint8_t* smem, int head) {
+                                         uint8_t* smem, int head, int rank) {
   using L = Layout<D>;
+  constexpr int kAccs = Q ? 1 : 2;
+  constexpr int kPartRow = D + 4;  // floats; the pad spreads the rows over the banks
+  static_assert(2 * kT * kPartRow * 4 <= L::kRows, "a cluster's partial sums reuse the tiles' shared memory");
   Ctl& ctl = *reinterpret_cast<Ctl*>(smem + L::kCtl);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const Unit u = ctl.u;
   const int nt = (u.S + kT - 1) / kT;  // tiles of the sequence
   const int group = p.num_heads / p.num_kv_heads;
+  const int split = p.split[Q ? 1 : 0];
   volatile int* abort_flag = &ctl.abort_flag;
   const uint32_t tmem = ctl.tmem_base;
   auto a_full = [&](int i) { return smem_u32(&ctl.a_full[i]); };
@@ -353,6 +379,10 @@ __device__ __forceinline__ void run_role(const CUtensorMap* tmFixA, const CUtens
       const int ring_head = Q ? head / group : head * group + step / chunks;
       uint32_t keep = ~next;
       if (nt - base < 32) keep &= (1u << (nt - base)) - 1u;
+      if (split > 1) {  // this rank's tiles: every split-th of the block's walk
+        const uint32_t every = split == 2 ? 0x55555555u : (split == 4 ? 0x11111111u : 0x01010101u);
+        keep &= every << ((rank - ((step / chunks) * nt + base)) & (split - 1));
+      }
       next = skipped(step + 1);
       if (lane == 0) {
         for (; keep && ok; keep &= keep - 1) {
@@ -600,21 +630,26 @@ __device__ __forceinline__ void run_role(const CUtensorMap* tmFixA, const CUtens
       const int heads = Q ? p.num_heads : p.num_kv_heads;
       const int64_t at = (static_cast<int64_t>(u.start + u.block * kT + row) * heads + head) * D + half * (D / 2);
 #pragma unroll
-      for (int a = 0; a < (Q ? 1 : 2); ++a) {
+      for (int a = 0; a < kAccs; ++a) {
         __nv_bfloat16* dst = (Q ? p.dq : (a ? p.dv : p.dk)) + at;
         const float f = a ? 1.f : p.scale;
 #pragma unroll
         for (int ch = 0; ch < D / 64; ++ch) {
           uint32_t o[32];
           tmem_ld_x32(lanes + (a ? kColAccB : kColAccA) + half * (D / 2) + ch * 32, o);
-          if (row_valid) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) o[i] = any ? o[i] : 0u;
+          if (split > 1) {
+            uint4* part = reinterpret_cast<uint4*>(smem + ((a * kT + row) * kPartRow + half * (D / 2) + ch * 32) * 4);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) part[i] = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+          } else if (row_valid) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               uint32_t w[4];
 #pragma unroll
               for (int k = 0; k < 4; ++k)
-                w[k] = any ? pack_bf16x2(__uint_as_float(o[8 * i + 2 * k]) * f, __uint_as_float(o[8 * i + 2 * k + 1]) * f)
-                           : 0u;
+                w[k] = pack_bf16x2(__uint_as_float(o[8 * i + 2 * k]) * f, __uint_as_float(o[8 * i + 2 * k + 1]) * f);
               reinterpret_cast<uint4*>(dst + ch * 32)[i] = make_uint4(w[0], w[1], w[2], w[3]);
             }
           }
@@ -622,10 +657,53 @@ __device__ __forceinline__ void run_role(const CUtensorMap* tmFixA, const CUtens
       }
     }
   }
+
+  if (split > 1) {  // the cluster's CTAs each add up a share of the rows
+    __syncwarp();
+    cluster_sync();
+    if (warp >= kEwWarp) {
+      const int heads = Q ? p.num_heads : p.num_kv_heads;
+      const int r0 = rank * (kT / split);
+      constexpr int kWords = D / 4;  // float4 per row
+      // Two words at a time, the loads of all ranks before their sums: a remote
+      // load takes hundreds of cycles.
+      const int words = kAccs * (kT / split) * kWords;
+      for (int i0 = threadIdx.x - 32 * kEwWarp; i0 < words; i0 += 2 * kEwThreads) {
+        float4 v[2][8];
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+          const int i = min(i0 + n * kEwThreads, words - 1);
+          const int word = i % kWords, a = i / kWords / (kT / split), row = r0 + i / kWords % (kT / split);
+          const uint32_t part = smem_u32(smem + ((a * kT + row) * kPartRow + word * 4) * 4);
+#pragma unroll
+          for (int c = 0; c < 8; ++c)
+            if (c < split) v[n][c] = ld_cluster(part, c);
+        }
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+          const int i = i0 + n * kEwThreads;
+          const int word = i % kWords, a = i / kWords / (kT / split), row = r0 + i / kWords % (kT / split);
+          float4 sum = v[n][0];
+#pragma unroll
+          for (int c = 1; c < 8; ++c)
+            if (c < split) sum.x += v[n][c].x, sum.y += v[n][c].y, sum.z += v[n][c].z, sum.w += v[n][c].w;
+          if (i < words && u.block * kT + row < u.S) {
+            const float f = a ? 1.f : p.scale;
+            __nv_bfloat16* dst = (Q ? p.dq : (a ? p.dv : p.dk)) +
+                                 (static_cast<int64_t>(u.start + u.block * kT + row) * heads + head) * D + word * 4;
+            *reinterpret_cast<uint2*>(dst) =
+                make_uint2(pack_bf16x2(sum.x * f, sum.y * f), pack_bf16x2(sum.z * f, sum.w * f));
+          }
+        }
+      }
+    }
+    cluster_sync();  // no CTA leaves while another still reads its shared memory
+  }
 }
 
 // blockIdx.x: 128-row block of the batch; blockIdx.y: the K/V heads (kv role,
-// the longer one, first), then the query heads (q role).
+// the longer one, first), then the query heads (q role), each as often as the
+// role is split. A cluster spans blockIdx.y.
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
     bwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
@@ -670,10 +748,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
 
-  if (y < p.num_kv_heads)
-    run_role<D, false>(&tmK, &tmV, &tmQ, &tmdO, p, smem, y);
+  const int kv_ctas = p.num_kv_heads * p.split[0];
+  if (y < kv_ctas)
+    run_role<D, false>(&tmK, &tmV, &tmQ, &tmdO, p, smem, y / p.split[0], y % p.split[0]);
   else
-    run_role<D, true>(&tmQ, &tmdO, &tmK, &tmV, p, smem, y - p.num_kv_heads);
+    run_role<D, true>(&tmQ, &tmdO, &tmK, &tmV, p, smem, (y - kv_ctas) / p.split[1], (y - kv_ctas) % p.split[1]);
 
   __syncwarp();
   tc_fence_before();
@@ -689,7 +768,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 int64_t bound_units(int total_tokens, int batch) { return (static_cast<int64_t>(total_tokens) + kT - 1) / kT + batch; }
 
 template <int D>
-int launch(const Params& p, const void* q, const void* k, const void* v, cudaStream_t stream) {
+int launch(Params p, const void* q, const void* k, const void* v, cudaStream_t stream) {
   CUtensorMap tq, tk, tv, tdo;
   if (!internal::bf16_tensor_map(&tq, q, p.total_tokens, p.num_heads, D) ||
       !internal::bf16_tensor_map(&tk, k, p.total_tokens, p.num_kv_heads, D) ||
@@ -699,12 +778,49 @@ int launch(const Params& p, const void* q, const void* k, const void* v, cudaStr
   constexpr int smem = Layout<D>::kAlloc;
   cudaError_t e = cudaFuncSetAttribute(bwd_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return internal::fail(e);
+  // Blocks are split as long as all CTAs still run at once (us, D = 128 unless
+  // said, unsplit / split: 1024 tokens of 2 heads, D = 64, 21.3 / 15.5 in 4;
+  // 1024 tokens of 8 query heads over 2 K/V heads 66.1 / 30.8 in 4, over one
+  // 117.4 / 37.7 in 8). Beyond that a split costs (2048 tokens of 8 heads 69.1 / 80.6 in
+  // 2), except where several query heads to a K/V head make the kv role's walk
+  // longer than a fair share of the work: then that role alone is split.
+  int split = 1, q_split = 1;
+  const int64_t kv_blocks = static_cast<int64_t>(p.units) * p.num_kv_heads;
+  const int64_t q_blocks = static_cast<int64_t>(p.units) * p.num_heads;
+  const int64_t group = p.num_heads / p.num_kv_heads;
+  const int64_t tiles = (static_cast<int64_t>(p.max_seqlen) + kT - 1) / kT;
+  // Per tile the kv role takes about 7/5 of the q role's time.
+  const bool long_walk = 7 * group * tiles * kSMs > (7 * group * kv_blocks + 5 * q_blocks) * tiles;
+  for (int s = 2; s <= 8 && s <= group * tiles; s *= 2) {
+    const bool heads_fill = p.num_heads % s == 0;  // clusters of whole q role blocks
+    if ((kv_blocks + q_blocks) * s <= kSMs) {
+      split = q_split = s;
+    } else if (heads_fill && (kv_blocks * s + q_blocks <= kSMs ||
+                              (s <= group && long_walk && 4 * kv_blocks * s <= 5 * kSMs))) {
+      split = s;
+      q_split = 1;
+    } else {
+      break;
+    }
+  }
+  p.split[0] = split;
+  p.split[1] = q_split;
   const unsigned units = static_cast<unsigned>(p.units);
   rows_kernel<D><<<dim3(units, static_cast<unsigned>(p.num_heads)), 256, 0, stream>>>(p);
   if ((e = cudaGetLastError()) != cudaSuccess) return internal::fail(e);
-  bwd_kernel<D><<<dim3(units, static_cast<unsigned>(p.num_heads + p.num_kv_heads)), kThreads, smem, stream>>>(
-      tq, tk, tv, tdo, p);
-  e = cudaGetLastError();
+  cudaLaunchConfig_t config{};
+  config.gridDim = dim3(units, static_cast<unsigned>(p.num_kv_heads * p.split[0] + p.num_heads * p.split[1]));
+  config.blockDim = dim3(kThreads);
+  config.dynamicSmemBytes = smem;
+  config.stream = stream;
+  cudaLaunchAttribute cluster{};
+  cluster.id = cudaLaunchAttributeClusterDimension;
+  cluster.val.clusterDim.x = 1;
+  cluster.val.clusterDim.y = static_cast<unsigned>(split);
+  cluster.val.clusterDim.z = 1;
+  config.attrs = &cluster;
+  config.numAttrs = split > 1 ? 1 : 0;
+  e = cudaLaunchKernelEx(&config, bwd_kernel<D>, tq, tk, tv, tdo, p);
   return e == cudaSuccess ? SSA_OK : internal::fail(e);
 }
 
@@ -752,6 +868,7 @@ int internal::launch_backward(const Backward& a, cudaStream_t stream) {
   p.rows = static_cast<float*>(a.workspace);
   p.batch = a.batch;
   p.total_tokens = a.total_tokens;
+  p.max_seqlen = a.max_seqlen;
   p.num_heads = a.num_heads;
   p.num_kv_heads = a.num_kv_heads;
   p.max_tiles = static_cast<int>((static_cast<int64_t>(a.max_seqlen) + kT - 1) / kT);

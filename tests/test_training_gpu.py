@@ -97,6 +97,33 @@ def test_bwd_formula(ssa, lens, H, Hk, D):
         ref.check(g, w, b, name)
 
 
+@pytest.mark.parametrize("lens,H,Hk,D", [([1300, 1], 16, 16, 64), ([1300, 1], 16, 8, 128), ([700], 24, 12, 64),
+                                         ([2000], 3, 3, 128), ([1030], 1, 1, 128), ([400] * 3, 16, 16, 128)], ids=str)
+def test_bwd_whole_and_shared_blocks(ssa, lens, H, Hk, D):
+    """Batches whose blocks are walked by one CTA each, or by clusters of 2, 4 and 8."""
+    q, k, v, dout, cu = make(lens, H, Hk, D, seed=20)
+    out, lse = ssa.fwd_lse(q, k, v, cu, max(lens))
+    grads = ssa.bwd(dout, q, k, v, out, lse, cu, max(lens))
+    ssa.check_device()
+    want, bound = ref.backward(dout, q, k, v, out, lse, lens)
+    for g, w, b, name in zip(grads, want, bound, ("dq", "dk", "dv")):
+        ref.check(g, w, b, name)
+
+
+@pytest.mark.parametrize("S,H,D,times", [(5120, 24, 128, 20), (4096, 12, 64, 40), (640, 4, 64, 100)])
+def test_bwd_waits_end(ssa, S, H, D, times):
+    """Many passes over long walks: no wait of the kernel's pipeline is missed
+    (a barrier that goes round unseen would run into the time limit), and
+    every pass gives the same bits."""
+    q, k, v, dout, cu = make([S], H, H, D, seed=21)
+    out, lse = ssa.fwd_lse(q, k, v, cu, S)
+    first = ssa.bwd(dout, q, k, v, out, lse, cu, S)
+    for _ in range(times):
+        again = ssa.bwd(dout, q, k, v, out, lse, cu, S)
+    ssa.check_device()
+    assert all(same(a, b) for a, b in zip(first, again))
+
+
 @pytest.mark.parametrize("D", [64, 128])
 @pytest.mark.parametrize("H,Hk", [(2, 2), (4, 2)])
 @pytest.mark.parametrize("scale", [0.0, 0.3])

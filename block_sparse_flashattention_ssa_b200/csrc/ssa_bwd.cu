@@ -9,6 +9,12 @@
 //   dQ_r  = c sum_j dS_rj k_j,  dK_j = c sum_r dS_rj q_r
 // The forward's decisions are constants: no gradient flows through them.
 //
+// P and dS are rounded to bf16 for their products, the precision the tensor
+// core takes Q, K and dO in; sums, statistics and D stay in fp32. Because
+// sum_j dS_rj is nearly zero, what the keys have in common cancels in dQ, but
+// not in its rounding errors: the q role sums up what the rounding of a row's
+// dS added and takes that times the mean key of its own block out again.
+//
 // A first kernel forms D and -L log2 e per row, padded to whole query blocks
 // (rows past a sequence end get -inf, so their probabilities vanish). The
 // main kernel's CTAs each own 128 output rows and walk the other side's tiles:
@@ -84,7 +90,7 @@ struct Params {
   const int32_t* cu_seqlens;
   const uint32_t* bitmap;  // forward's skip decisions, or NULL: every tile is kept
   __nv_bfloat16 *dq, *dk, *dv;
-  const __nv_bfloat16 *out, *dout;
+  const __nv_bfloat16 *out, *dout, *k, *v;
   const float* lse;
   float* rows;  // [num_heads][units][2][128]: -L log2 e, then -D, per query block
   int* status;
@@ -238,7 +244,10 @@ __device__ void locate(const Params& p, int x, int lane, bool report, Unit& u) {
 }
 
 // -D_r = -dO_r.O_r and -L_r log2 e of one query block and head; D / 8 lanes per
-// row, 16 bytes of dO and O each. Bound by the read of dO and O.
+// row, 16 bytes of dO and O each. Bound by the read of dO and O. The one row of
+// a sequence of length one gets dP - D = dO.(v - O) in place of -D: the forward
+// wrote O = v there, and the difference of two rounded dot products would be
+// all that is left of a gradient that is zero.
 template <int D>
 __global__ void __launch_bounds__(256) rows_kernel(const __grid_constant__ Params p) {
   __shared__ Unit u;
@@ -266,11 +275,17 @@ __global__ void __launch_bounds__(256) rows_kernel(const __grid_constant__ Param
   for (int i = 0; i < kSteps; ++i) {
     const int r = r0 + i * kRowsAtOnce;
     const uint32_t x[4] = {a[i].x, a[i].y, a[i].z, a[i].w}, y[4] = {b[i].x, b[i].y, b[i].z, b[i].w};
+    uint4 v4 = make_uint4(0, 0, 0, 0);
+    if (u.S == 1 && r == 0)
+      v4 = *reinterpret_cast<const uint4*>(
+          p.v + (static_cast<int64_t>(u.start) * p.num_kv_heads + head / (p.num_heads / p.num_kv_heads)) * D + part * 8);
+    const uint32_t z[4] = {v4.x, v4.y, v4.z, v4.w};
     float sum = 0.f;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      sum = fmaf(__uint_as_float(x[k] << 16), __uint_as_float(y[k] << 16), sum);
-      sum = fmaf(__uint_as_float(x[k] & 0xFFFF0000u), __uint_as_float(y[k] & 0xFFFF0000u), sum);
+      const float2 g = unpack_bf16x2(x[k]), o = unpack_bf16x2(y[k]), v = unpack_bf16x2(z[k]);
+      sum = fmaf(g.x, o.x - v.x, sum);
+      sum = fmaf(g.y, o.y - v.y, sum);
     }
 #pragma unroll
     for (int o = kLanes / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
@@ -292,6 +307,42 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
       "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
       "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(bar)
       : "memory");
+}
+
+// Mean of the keys of this block's rows, finite values only (the dQ of a row
+// that saw others is not finite anyway); eight warps take D / 8 columns each.
+template <int D>
+__device__ __forceinline__ void key_mean(const Params& p, const Unit& u, int head, int warp, int lane, float* mean) {
+  constexpr int kCols = D / 8;
+  const int rows = min(kT, u.S - u.block * kT);
+  float sum[kCols];
+#pragma unroll
+  for (int i = 0; i < kCols; ++i) sum[i] = 0.f;
+#pragma unroll
+  for (int n = 0; n < kT / 32; ++n) {
+    const int r = lane + n * 32;
+    if (r < rows) {
+      const __nv_bfloat16* k =
+          p.k + (static_cast<int64_t>(u.start + u.block * kT + r) * p.num_kv_heads + head) * D + warp * kCols;
+#pragma unroll
+      for (int i = 0; i < kCols / 8; ++i) {
+        const uint4 v = reinterpret_cast<const uint4*>(k)[i];
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const float2 f = unpack_bf16x2(w[c]);
+          sum[i * 8 + 2 * c] += isfinite(f.x) ? f.x : 0.f;
+          sum[i * 8 + 2 * c + 1] += isfinite(f.y) ? f.y : 0.f;
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < kCols; ++i) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum[i] += __shfl_xor_sync(kFull, sum[i], o);
+    if (lane == 0) mean[warp * kCols + i] = sum[i] / static_cast<float>(rows);
+  }
 }
 
 // All threads of the cluster; orders shared-memory accesses before it against
@@ -519,7 +570,12 @@ __device__ __forceinline__ void run_role(const CUtensorMap* tmFixA, const CUtens
     const uint32_t lanes = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
     const bool row_valid = u.block * kT + row < u.S;
     float row_bias = 0.f, row_ndelta = 0.f;  // q role: this thread's row
+    const float2 zero = make_float2(0.f, 0.f);
+    float2 exact[2] = {zero, zero}, rounded[2] = {zero, zero};  // q role: sums of its dS before and after rounding
+    float* mean_key = reinterpret_cast<float*>(smem + L::kRows);       // q role: [D], then the rows' sums [2][128]
     if (Q) {
+      key_mean<D>(p, u, head / group, warp - kEwWarp, lane, mean_key);
+      named_barrier_sync(1, kEwThreads);
       const float* r = p.rows + (static_cast<int64_t>(head) * p.units + u.gqb0 + u.block) * (2 * kT);
       row_bias = r[row];
       row_ndelta = r[kT + row];
@@ -601,6 +657,7 @@ __device__ __forceinline__ void run_role(const CUtensorMap* tmFixA, const CUtens
 #pragma unroll
         for (int i = 0; i < 64; ++i)
           if (half * 64 + i >= valid) d[i] = 0u;
+        if (u.S == 1) d[0] = half == 0 ? 0u : d[0];  // -D holds dP - D (see rows_kernel)
       }
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
@@ -614,6 +671,12 @@ __device__ __forceinline__ void run_role(const CUtensorMap* tmFixA, const CUtens
                                      make_float2(n4.z, n4.w)));
         pk[2 * i] = pack_bf16x2(x.x, x.y);
         pk[2 * i + 1] = pack_bf16x2(y.x, y.y);
+        if (Q) {
+          exact[0] = fadd2(exact[0], x);
+          exact[1] = fadd2(exact[1], y);
+          add_bf16x2(rounded[0], pk[2 * i]);
+          add_bf16x2(rounded[1], pk[2 * i + 1]);
+        }
       }
       tmem_st_x32(lanes + col_s(j) + half * 64 + (Q ? 0 : 32), pk);
       warp_arrive(ds_full(j), lane);
@@ -624,6 +687,14 @@ __device__ __forceinline__ void run_role(const CUtensorMap* tmFixA, const CUtens
 
     // Epilogue: this thread's row and half of the D columns of each accumulator.
     const bool any = j > 0;  // no tile was kept: the gradients are zero
+    float excess = 0.f;      // q role: of the row, over both halves of its columns
+    if (Q) {                 // every element-wise warp comes here, with or without an error
+      float* sums = mean_key + D;
+      sums[half * kT + row] = ((rounded[0].x - exact[0].x) + (rounded[0].y - exact[0].y)) +
+                               ((rounded[1].x - exact[1].x) + (rounded[1].y - exact[1].y));
+      named_barrier_sync(1, kEwThreads);
+      excess = sums[row] + sums[kT + row];
+    }
     if (ok) ok = warp_wait(acc_full, 0, abort_flag, p.status);
     if (ok) {
       tc_fence_after();
@@ -638,7 +709,11 @@ __device__ __forceinline__ void run_role(const CUtensorMap* tmFixA, const CUtens
           uint32_t o[32];
           tmem_ld_x32(lanes + (a ? kColAccB : kColAccA) + half * (D / 2) + ch * 32, o);
 #pragma unroll
-          for (int i = 0; i < 32; ++i) o[i] = any ? o[i] : 0u;
+          for (int i = 0; i < 32; ++i) {
+            float x = any ? __uint_as_float(o[i]) : 0.f;
+            if (Q) x = fmaf(-excess, mean_key[half * (D / 2) + ch * 32 + i], x);
+            o[i] = __float_as_uint(x);
+          }
           if (split > 1) {
             uint4* part = reinterpret_cast<uint4*>(smem + ((a * kT + row) * kPartRow + half * (D / 2) + ch * 32) * 4);
 #pragma unroll
@@ -864,6 +939,8 @@ int internal::launch_backward(const Backward& a, cudaStream_t stream) {
   p.dv = static_cast<__nv_bfloat16*>(a.dv);
   p.out = static_cast<const __nv_bfloat16*>(a.out);
   p.dout = static_cast<const __nv_bfloat16*>(a.dout);
+  p.k = static_cast<const __nv_bfloat16*>(a.k);
+  p.v = static_cast<const __nv_bfloat16*>(a.v);
   p.lse = a.lse;
   p.rows = static_cast<float*>(a.workspace);
   p.batch = a.batch;

@@ -95,7 +95,7 @@ def backward(dout, q, k, v, out, lse, lens, bitmap=None, scale=0.0):
         dS = P * (dP - delta)
         rho = err + 8 * E * (s.abs().where(P > 0, torch.zeros_like(s)) + L.abs().where(~torch.isinf(L), torch.zeros_like(L))[:, None] + 1)
         eP = P * rho                                      # fp32 P
-        eS = eP * (dP - delta).abs() + (P + eP) * (D + 2) * E * (dO.abs() @ V.abs().T + (dO.abs() * O.abs()).sum(1, keepdim=True))
+        eS = (eP * (dP - delta).abs() + (P + eP) * (D + 2) * E * (dO.abs() @ V.abs().T + (dO.abs() * O.abs()).sum(1, keepdim=True)))
         rP, rS = eP + U * (P + eP), eS + U * (dS.abs() + eS)  # after rounding to bf16
         N = n * G
         dv[lo:hi, g] += P.T @ dO
@@ -103,7 +103,12 @@ def backward(dout, q, k, v, out, lse, lens, bitmap=None, scale=0.0):
         dk[lo:hi, g] += c * (dS.T @ Q)
         bk[lo:hi, g] += c * (rS.T @ Q.abs() + N * E * ((dS.abs() + rS).T @ Q.abs()))
         dq[lo:hi, h] = c * (dS @ K)
-        bq[lo:hi, h] = c * (rS @ K.abs() + n * E * ((dS.abs() + rS) @ K.abs()))
+        # What rounding adds to a row's dS, times a mean of finite keys, is taken
+        # out of dQ: its error is sum_j e_j (k_j - m) with |e_j| <= U (|dS_j| + ..),
+        # at most sum_j |e_j| (|k_j| + |m|), and |m| is at most the largest |k|.
+        m = K.abs().where(torch.isfinite(K), torch.zeros_like(K)).amax(0)
+        bq[lo:hi, h] = c * (rS @ K.abs() + n * E * ((dS.abs() + rS) @ K.abs())
+                            + (1 + n * E) * U * ((dS.abs() + eS).sum(1, keepdim=True) * m))
     fin = lambda x, b: b + (U + 4 * E) * (x.abs() + b) + 1e-37  # the scale in fp32 and the rounding of the result
     return (dq, dk, dv), (fin(dq, bq), fin(dk, bk), fin(dv, bv))
 

@@ -196,9 +196,12 @@ __global__ void __launch_bounds__(kThreads, 4) rotary_kernel(const __grid_consta
 
 template <bool INTERLEAVED, int N>
 int launch(const Params& p, cudaStream_t stream) {
-  // Enough tokens per CTA that a thread has two batches of 16-byte pieces.
+  // Enough tokens per CTA that a thread has two batches of 16-byte pieces, or
+  // four where that still makes 16 CTAs per SM (75,600 x 40 + 40 x 128
+  // interleaved 497 / 465 us, with one batch 579; 8192 x 24 + 24 39.5 / 40.0).
   const int per_token = (p.heads[0] + p.heads[1]) * (p.dim / 8);
-  int n = (8 * kThreads + per_token - 1) / per_token;
+  int n = (16 * kThreads + per_token - 1) / per_token;
+  if (p.tokens / n < 148 * 16) n = (8 * kThreads + per_token - 1) / per_token;
   n = n < 1 ? 1 : (n > 16 ? 16 : n);
   const unsigned blocks = static_cast<unsigned>((static_cast<int64_t>(p.tokens) + n - 1) / n);
   const size_t smem = static_cast<size_t>(n) * (p.rot / 2 + 3) * sizeof(float2);  // + 3: the last piece's unused pairs

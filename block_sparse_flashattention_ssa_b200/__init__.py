@@ -381,6 +381,12 @@ def _may(t, name, dtype, dev, shape):
         _need(t, name, dtype, dev, shape)
 
 
+def _current_handle(torch, dev):
+    """The current stream's cudaStream_t, without a Stream object where torch can."""
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return raw(dev.index) if raw is not None else torch.cuda.current_stream(dev).cuda_stream
+
+
 def _run(dev, stream, tensors, body):
     """``body(stream handle)`` with ``dev`` current and on ``stream`` (default:
     the device's current one), so that what it allocates belongs to the stream
@@ -388,11 +394,11 @@ def _run(dev, stream, tensors, body):
     reuse until both that stream and the caller's are done with them."""
     import torch
 
-    current = torch.cuda.current_stream(dev)
     here = torch.cuda.current_device() == dev.index
-    if stream is None or (here and stream == current):
-        if here:
-            return body(current.cuda_stream)
+    if stream is None and here:
+        return body(_current_handle(torch, dev))
+    current = torch.cuda.current_stream(dev)
+    if stream is None or stream == current:
         stream = current
     elif stream.device != dev:
         raise ValueError(f"stream is on {stream.device}, the tensors on {dev}")
@@ -650,6 +656,27 @@ def _rows_overlap(a, a_stride, b, b_stride):
     return d < wa or d + wb > sa
 
 
+def _check_rotary_outputs(dev, total, dim, inputs, xs, outputs, ys):
+    """Checks of rotary's given outputs; fills in their token strides."""
+    written = []
+    for i, (o, x, name) in enumerate(zip(outputs, inputs, ("out_q", "out_k"))):
+        if o is None:
+            continue
+        if x is None:
+            raise ValueError("out_k without k")
+        ys[i] = _rows(o, name, dev, total, dim)
+        if o.shape != x.shape:
+            raise ValueError(f"{name} has shape {tuple(o.shape)}, expected {tuple(x.shape)}")
+        written.append((o, ys[i]))
+        for y, stride, other in zip(inputs, xs, ("q", "k")):
+            if y is None or (y is x and o.data_ptr() == x.data_ptr() and ys[i] == stride):
+                continue  # in place: a pair is read and written by one thread
+            if _rows_overlap(o, ys[i], y, stride):
+                raise ValueError(f"{name} overlaps {other}")
+    if len(written) == 2 and _rows_overlap(*written[0], *written[1]):
+        raise ValueError("out_q overlaps out_k")
+
+
 def rotary(q, k, positions, inv_freq, sections=None, interleaved: bool = False, scale: float = 1.0,
            transpose: bool = False, out_q=None, out_k=None, stream=None):
     """Rotary positions on Q and, unless it is None, on K, in one launch.
@@ -682,31 +709,16 @@ def rotary(q, k, positions, inv_freq, sections=None, interleaved: bool = False, 
     counts = [pairs] if sections is None else [int(n) for n in sections]
     if len(counts) != axes or min(counts) < 0 or sum(counts) != pairs:
         raise ValueError(f"sections must be {axes} counts adding up to {pairs}")
-    Hk = 0 if k is None else k.shape[1]
     xs = [_rows(q, "q", dev, total, D), 0 if k is None else _rows(k, "k", dev, total, D)]
+    Hk = 0 if k is None else k.shape[1]
     ys = [H * D, Hk * D]
-    written = []
-    for i, (o, name, x) in enumerate(((out_q, "out_q", q), (out_k, "out_k", k))):
-        if o is None:
-            continue
-        if x is None:
-            raise ValueError("out_k without k")
-        ys[i] = _rows(o, name, dev, total, D)
-        if o.shape != x.shape:
-            raise ValueError(f"{name} has shape {tuple(o.shape)}, expected {tuple(x.shape)}")
-        written.append((o, ys[i], name))
-        for y, stride, other in ((q, xs[0], "q"), (k, xs[1], "k")):
-            if y is None or (y is x and o.data_ptr() == x.data_ptr() and ys[i] == stride):
-                continue  # in place: a pair is read and written by one thread
-            if _rows_overlap(o, ys[i], y, stride):
-                raise ValueError(f"{name} overlaps {other}")
-    if len(written) == 2 and _rows_overlap(written[0][0], written[0][1], written[1][0], written[1][1]):
-        raise ValueError("out_q overlaps out_k")
+    if out_q is not None or out_k is not None:
+        _check_rotary_outputs(dev, total, D, (q, k), xs, (out_q, out_k), ys)
     n_pairs = _sections_type(axes)(*counts)
 
     def body(handle):
         oq = torch.empty_like(q, memory_format=torch.contiguous_format) if out_q is None else out_q
-        ok = torch.empty_like(k, memory_format=torch.contiguous_format) if out_k is None and Hk else out_k
+        ok = torch.empty_like(k, memory_format=torch.contiguous_format) if out_k is None and k is not None else out_k
         _check(_lib.ssa_rotary(_at(q), _at(k), _at(oq), _at(ok), xs[0], xs[1], ys[0], ys[1], total, H, Hk, D,
                                _at(positions), axes, n_pairs, _at(inv_freq), 2 * pairs, 1 if interleaved else 0,
                                float(scale), 1 if transpose else 0, handle), "ssa_rotary")

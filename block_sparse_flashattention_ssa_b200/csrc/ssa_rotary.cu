@@ -51,6 +51,17 @@ __device__ __forceinline__ uint32_t pack(float lo, float hi) {
 __device__ __forceinline__ float low(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float high(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 
+// (cos, sin) of pair j at a token, with the scale and the direction.
+__device__ __forceinline__ float2 table_entry(const Params& p, int64_t token, int j) {
+  int axis = 0;
+  while (axis < p.axes - 1 && j >= p.axis_end[axis]) ++axis;
+  const double pos = static_cast<double>(p.positions[token * p.axes + axis]);
+  const double turns = pos * (p.inv_freq[j] * 0.15915494309189533577);  // 1 / 2 pi
+  float s, c;
+  sincospif(2.f * static_cast<float>(turns - rint(turns)), &s, &c);
+  return make_float2(c * p.scale, s * p.scale * p.sign);
+}
+
 // N consecutive elements of a head, moved with one access of 2 N bytes.
 template <int N>
 struct Piece;
@@ -111,15 +122,9 @@ __global__ void __launch_bounds__(kThreads, 4) rotary_kernel(const __grid_consta
   const int nt = static_cast<int>(min(static_cast<int64_t>(tokens_per_cta), p.tokens - t0));
   for (int i = threadIdx.x; i < nt * pairs; i += kThreads) {
     const int t = i / pairs, j = i - t * pairs;
-    int axis = 0;
-    while (axis < p.axes - 1 && j >= p.axis_end[axis]) ++axis;
-    const double pos = static_cast<double>(p.positions[(t0 + t) * p.axes + axis]);
-    const double turns = pos * (p.inv_freq[j] * 0.15915494309189533577);  // 1 / 2 pi
-    float s, c;
-    sincospif(2.f * static_cast<float>(turns - rint(turns)), &s, &c);
     const int piece = j / kPairs, k = j % kPairs;
     const int at = kPairs == 1 ? j : ((k / 2) * turned + piece) * 2 + (k & 1);
-    table[t * row_table + at] = make_float2(c * p.scale, s * p.scale * p.sign);
+    table[t * row_table + at] = table_entry(p, t0 + t, j);
   }
   __syncthreads();
 
@@ -194,15 +199,110 @@ __global__ void __launch_bounds__(kThreads, 4) rotary_kernel(const __grid_consta
   }
 }
 
-template <bool INTERLEAVED, int N>
-int launch(const Params& p, cudaStream_t stream) {
-  // Enough tokens per CTA that a thread has two batches of 16-byte pieces, or
-  // four where that still makes 16 CTAs per SM (75,600 x 40 + 40 x 128
-  // interleaved 497 / 465 us, with one batch 579; 8192 x 24 + 24 39.5 / 40.0).
+// The half layout where rot / 2 is odd, so that the elements of pairs suit no
+// access wider than one, but the rows are 16-byte aligned (DIM 64, 128 or 256):
+// a warp brings whole heads into shared memory with 16-byte loads and turns
+// them there, a 32-bit word (two elements, each with a partner rot / 2 away on
+// one side or the other) per lane at a time. 20,000 x 16 + 16 x 128, rot 126:
+// 98 us, element by element 169; with rot / 2 even, two elements at a time, the
+// kernel above takes 88 and this one 98.
+template <int DIM>
+__global__ void __launch_bounds__(kThreads, 4) rotary_words_kernel(const __grid_constant__ Params p,
+                                                                   int tokens_per_cta) {
+  extern __shared__ __align__(16) float2 table[];  // [tokens_per_cta][pairs]
+  constexpr int kPieces = DIM / 8, kHeads = 32 / kPieces;  // 16-byte pieces of a head, heads a warp takes at once
+  constexpr int kBatch = 4, kWarps = kThreads / 32;
+  __shared__ __align__(16) uint4 staged[kWarps][kBatch][32];
+  const int pairs = p.rot / 2;
+  const int64_t t0 = static_cast<int64_t>(blockIdx.x) * tokens_per_cta;
+  const int nt = static_cast<int>(min(static_cast<int64_t>(tokens_per_cta), p.tokens - t0));
+  for (int i = threadIdx.x; i < nt * pairs; i += kThreads) {
+    const int t = i / pairs;
+    table[i] = table_entry(p, t0 + t, i - t * pairs);
+  }
+  __syncthreads();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int heads = p.heads[0] + p.heads[1], rows = nt * heads;
+  for (int first = warp * kHeads * kBatch; first < rows; first += kWarps * kHeads * kBatch) {
+    uint4 v[kBatch];
+    int token = (first + lane / kPieces) / heads, head = (first + lane / kPieces) - token * heads;
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) {
+      if (token < nt) {
+        const int which = head >= p.heads[0] ? 1 : 0;
+        v[b] = __ldcs(reinterpret_cast<const uint4*>(p.x[which] + (t0 + token) * p.xs[which] +
+                                                     static_cast<int64_t>(head - (which ? p.heads[0] : 0)) * DIM) +
+                      lane % kPieces);
+      }
+      head += kHeads;
+      while (head >= heads) {
+        head -= heads;
+        ++token;
+      }
+    }
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) staged[warp][b][lane] = v[b];
+    __syncwarp();
+    token = first / heads;
+    head = first - token * heads;
+#pragma unroll
+    for (int r = 0; r < kBatch * kHeads; ++r) {  // the warp's heads in turn
+      if (token < nt) {
+        const int which = head >= p.heads[0] ? 1 : 0;
+        uint32_t* y = reinterpret_cast<uint32_t*>(p.y[which] + (t0 + token) * p.ys[which] +
+                                                  static_cast<int64_t>(head - (which ? p.heads[0] : 0)) * DIM);
+        const unsigned short* x = reinterpret_cast<const unsigned short*>(&staged[warp][0][0]) + r * DIM;
+        const float2* cs = table + token * pairs;
+#pragma unroll
+        for (int k = 0; k < DIM / 64; ++k) {
+          const int word = lane + 32 * k, e = 2 * word;
+          const uint32_t own = reinterpret_cast<const uint32_t*>(x)[word];
+          uint32_t w = own;
+          if (e < p.rot) {
+            // Left elements of pairs have their partner to the right, and the
+            // other way round; the two elements of a word may differ in that.
+            const bool l0 = e < pairs, l1 = e + 1 < pairs;
+            const float o0 = low(x[l0 ? e + pairs : e - pairs]), o1 = low(x[l1 ? e + 1 + pairs : e + 1 - pairs]);
+            const float2 c0 = cs[l0 ? e : e - pairs], c1 = cs[l1 ? e + 1 : e + 1 - pairs];
+            float a0, b0, a1, b1;
+            turn_pair(l0 ? low(own) : o0, l0 ? o0 : low(own), c0, a0, b0);
+            turn_pair(l1 ? high(own) : o1, l1 ? o1 : high(own), c1, a1, b1);
+            w = pack(l0 ? a0 : b0, l1 ? a1 : b1);
+          }
+          __stcs(y + word, w);
+        }
+      }
+      if (++head == heads) {
+        head = 0;
+        ++token;
+      }
+    }
+    __syncwarp();
+  }
+}
+
+// Tokens per CTA: a thread gets two batches of 16-byte pieces, or four where
+// that still makes 16 CTAs per SM (75,600 x 40 + 40 x 128 interleaved 497 / 465
+// us, with one batch 579; 8192 x 24 + 24 39.5 / 40.0).
+int tokens_of_cta(const Params& p) {
   const int per_token = (p.heads[0] + p.heads[1]) * (p.dim / 8);
   int n = (16 * kThreads + per_token - 1) / per_token;
   if (p.tokens / n < 148 * 16) n = (8 * kThreads + per_token - 1) / per_token;
-  n = n < 1 ? 1 : (n > 16 ? 16 : n);
+  return n < 1 ? 1 : (n > 16 ? 16 : n);
+}
+
+template <int DIM>
+int launch_words(const Params& p, cudaStream_t stream) {
+  const int n = tokens_of_cta(p);
+  const unsigned blocks = static_cast<unsigned>((static_cast<int64_t>(p.tokens) + n - 1) / n);
+  rotary_words_kernel<DIM><<<blocks, kThreads, static_cast<size_t>(n) * (p.rot / 2) * sizeof(float2), stream>>>(p, n);
+  const cudaError_t e = cudaGetLastError();
+  return e == cudaSuccess ? SSA_OK : internal::fail(e);
+}
+
+template <bool INTERLEAVED, int N>
+int launch(const Params& p, cudaStream_t stream) {
+  const int n = tokens_of_cta(p);
   const unsigned blocks = static_cast<unsigned>((static_cast<int64_t>(p.tokens) + n - 1) / n);
   const size_t smem = static_cast<size_t>(n) * (p.rot / 2 + 3) * sizeof(float2);  // + 3: the last piece's unused pairs
   rotary_kernel<INTERLEAVED, N><<<blocks, kThreads, smem, stream>>>(p, n);
@@ -248,17 +348,18 @@ extern "C" int ssa_rotary(const void* q, const void* k, void* q_out, void* k_out
   const int64_t xs[2] = {q_stride, k_stride}, ys[2] = {q_out_stride, k_out_stride};
   // Largest run of elements, up to 8, that suits every address and stride and,
   // in the half layout, the distance between the elements of a pair.
-  uint64_t steps = 8 | (interleaved ? 0 : static_cast<uint64_t>(rotary_dim / 2));
+  uint64_t aligned = 0;
   for (int i = 0; i < n; ++i) {
     const uintptr_t both = reinterpret_cast<uintptr_t>(in[i]) | reinterpret_cast<uintptr_t>(out[i]);
     if (both & 1u) return SSA_ERR_UNSUPPORTED;
-    steps |= both / 2 | static_cast<uint64_t>(xs[i]) | static_cast<uint64_t>(ys[i]);
+    aligned |= both / 2 | static_cast<uint64_t>(xs[i]) | static_cast<uint64_t>(ys[i]);
     p.x[i] = static_cast<const __nv_bfloat16*>(in[i]);
     p.y[i] = static_cast<__nv_bfloat16*>(out[i]);
     p.xs[i] = xs[i];
     p.ys[i] = ys[i];
     p.heads[i] = i ? num_kv_heads : num_heads;
   }
+  uint64_t steps = 8 | aligned | (interleaved ? 0 : static_cast<uint64_t>(rotary_dim / 2));
   steps &= ~steps + 1;  // its lowest set bit
   if (const int rc = internal::device_pointers({q, q_out, positions, rotary_dim > 0 ? inv_freq : nullptr,
                                                 n == 2 ? k : nullptr, n == 2 ? k_out : nullptr});
@@ -274,6 +375,11 @@ extern "C" int ssa_rotary(const void* q, const void* k, void* q_out, void* k_out
   p.sign = transpose ? -1.f : 1.f;
   const cudaStream_t on = static_cast<cudaStream_t>(stream);
   if (interleaved) return steps == 8 ? launch<true, 8>(p, on) : launch<true, 1>(p, on);
+  if (aligned % 8 == 0 && steps == 1) {
+    if (head_dim == 64) return launch_words<64>(p, on);
+    if (head_dim == 128) return launch_words<128>(p, on);
+    if (head_dim == 256) return launch_words<256>(p, on);
+  }
   switch (steps) {
     case 8: return launch<false, 8>(p, on);
     case 4: return launch<false, 4>(p, on);

@@ -330,7 +330,8 @@ def test_bwd_from_saved(ssa, H, Hk, D, tsf):
 # ------------------------------------------------------------------- rotary
 
 ROTARY = [(1, 1, 1, 8, 8, 1), (3, 2, 1, 64, 64, 1), (129, 5, 2, 128, 128, 3), (50, 3, 3, 64, 30, 1), (33, 1, 4, 128, 2, 2),
-          (17, 2, 2, 72, 56, 1), (10, 2, 1, 64, 0, 1), (1000, 24, 24, 128, 96, 3), (5, 2, 2, 256, 256, 4)]
+          (17, 2, 2, 72, 56, 1), (10, 2, 1, 64, 0, 1), (1000, 24, 24, 128, 96, 3), (5, 2, 2, 256, 256, 4),
+          (21, 3, 1, 256, 250, 2), (40, 2, 7, 128, 126, 1), (77, 1, 1, 128, 66, 1)]
 
 
 @pytest.mark.parametrize("T,H,Hk,D,rot,axes", ROTARY)
@@ -355,7 +356,7 @@ def test_rotary(ssa, T, H, Hk, D, rot, axes, interleaved, transpose):
 
 
 @pytest.mark.parametrize("interleaved", [False, True])
-@pytest.mark.parametrize("rot", [64, 60])
+@pytest.mark.parametrize("rot", [64, 62, 60])
 def test_rotary_slices_in_place_and_alone(ssa, interleaved, rot):
     """Q and K as slices of a fused projection, written in place, and Q alone."""
     from block_sparse_flashattention_ssa_b200 import positions as pos

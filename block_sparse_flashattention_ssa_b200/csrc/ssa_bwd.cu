@@ -40,15 +40,18 @@
 // drained the tensor pipe: 3280 and 2976 cycles per tile in the kv and q role.
 // TMEM (512 columns): two score regions X [0,128) and Y [128,256), accA
 // [256,256+D), and
-//   kv role: accB [384,384+D). Tile j has S in one score region and dP in the
-//            other; P and dS, as bf16 pairs, replace S once it is in registers
-//            (P in the first 32 of each 64 columns, dS in the second). S of the
-//            next tile takes the place of dP as soon as that has been read,
-//            and dP of the next tile that of P and dS once the products that
-//            read them are complete: the regions change places with every tile.
-//   q role:  S in X and Z [384,512) by turns, dP in Y; dS replaces S. S of a
-//            tile is formed as soon as dQ has taken dS of the tile before last,
-//            dP as soon as the last tile's has been read.
+//   kv role, D = 128: accB [384,512). Tile j has S in one score region and dP
+//            in the other; P and dS, as bf16 pairs, replace S once it is in
+//            registers (P in the first 32 of each 64 columns, dS in the
+//            second). S of the next tile takes the place of dP as soon as that
+//            has been read, and dP of the next tile that of P and dS once the
+//            products that read them are complete: the regions change places
+//            with every tile.
+//   q role, and kv role with D = 64 (accB [320,384)): S in X and Z [384,512) by
+//            turns, dP in Y; dS (and P) replace S. S of a tile is formed as
+//            soon as P and dS of the tile before last are used, dP as soon as
+//            the last tile's has been read.
+//
 // Every wait is bounded in time; one that runs out records SSA_ERR_TIMEOUT in
 // the status word, the other roles leave at their next wait, in-flight loads
 // and MMAs are drained and TMEM is released.
@@ -81,7 +84,7 @@ constexpr int kThreads = 32 * kEwWarp + kEwThreads;
 constexpr int kAStages = 3;  // ring A lives from its S to its dS product, longer than ring B
 constexpr int kBStages = 2;
 constexpr uint32_t kTmemCols = 512;
-constexpr uint32_t kColX = 0, kColY = 128, kColAccA = 256, kColAccB = 384, kColZ = 384;
+constexpr uint32_t kColX = 0, kColY = 128, kColAccA = 256, kColZ = 384;  // accB: behind accA's D columns
 constexpr uint32_t kFull = 0xFFFFFFFFu;
 constexpr int kSMs = 148;
 constexpr float kLog2e = 1.44269504088896340736f;
@@ -113,8 +116,8 @@ struct Ctl {
   // MMA results ready: S of even and odd tiles, dP; element-wise warps: dP in
   // registers; P (kv role) and dS of even and odd tiles stored. Two barriers
   // where the side that completes them may be a tile ahead of the side that
-  // looks (the S issuer of the element-wise warps in the q role, these of the
-  // accumulating issuer): a single one would have gone round.
+  // looks (the S issuer of the element-wise warps with three score regions,
+  // these of the accumulating issuer): a single one would have gone round.
   uint64_t s_full[2], dp_full, dp_done, p_full[2], ds_full[2];
   uint64_t acc_full, drain[3];
   uint32_t tmem_base;
@@ -368,6 +371,8 @@ __device__ __forceinline__ void run_role(const CUtensorMap* tmFixA, const CUtens
                                          uint8_t* smem, int head, int rank) {
   using L = Layout<D>;
   constexpr int kAccs = Q ? 1 : 2;
+  constexpr bool kThree = Q || D == 64;           // three score regions; else two, which change places
+  constexpr uint32_t kColAccB = kColAccA + D;     // kv role
   constexpr int kPartRow = D + 4;  // floats; the pad spreads the rows over the banks
   static_assert(2 * kT * kPartRow * 4 <= L::kRows, "a cluster's partial sums reuse the tiles' shared memory");
   Ctl& ctl = *reinterpret_cast<Ctl*>(smem + L::kCtl);
@@ -391,8 +396,8 @@ __device__ __forceinline__ void run_role(const CUtensorMap* tmFixA, const CUtens
   // its P and dS, and (kv role) its ring B stage and row values, are complete.
   auto acc_done = [&](int j) { return smem_u32(&ctl.a_empty[j % kAStages]); };  // phase j / kAStages
   // The region of S of tile j, then of its dS and (kv role) P; and that of dP.
-  auto col_s = [&](int j) { return j & 1 ? (Q ? kColZ : kColY) : kColX; };
-  auto col_dp = [&](int j) { return Q || !(j & 1) ? kColY : kColX; };
+  auto col_s = [&](int j) { return j & 1 ? (kThree ? kColZ : kColY) : kColX; };
+  auto col_dp = [&](int j) { return kThree || !(j & 1) ? kColY : kColX; };
 
   if (warp == kTmaWarp) {
     // ------------------------------------------------------------ producer
@@ -521,22 +526,23 @@ __device__ __forceinline__ void run_role(const CUtensorMap* tmFixA, const CUtens
         return ok && *static_cast<volatile int*>(&ctl.info[j % kAStages]) >= 0;
       };
       if (warp == kSWarp) {
-        // S(j), once dS(j-2) is used (q role) or dP(j-1) has been read (kv role).
+        // S(j), once P and dS of tile j-2 are used (three regions) or dP(j-1) has been read (two).
         ok = wait(fix_full, 0);
         for (int j = 0; ok && has(j); ++j) {
-          if (Q ? j > 1 && !(ok = wait(acc_done(j - 2), ((j - 2) / kAStages) & 1))
-                : j > 0 && !(ok = wait(dp_done, (j - 1) & 1)))
+          if (kThree ? j > 1 && !(ok = wait(acc_done(j - 2), ((j - 2) / kAStages) & 1))
+                     : j > 0 && !(ok = wait(dp_done, (j - 1) & 1)))
             break;
           tc_fence_after();
           product(col_s(j), L::kFixA, ring_a(j));
           tc_commit(s_full(j));
         }
       } else if (warp == kDPWarp) {
-        // dP(j), once dP(j-1) has been read (q role), or P and dS of tile j-1 (kv role) used.
+        // dP(j), once dP(j-1) has been read (three regions), or P and dS of tile j-1 used (two).
         ok = wait(fix_full, 0);
         for (int j = 0; ok && has(j); ++j) {
           if (!(ok = wait(b_full(j % kBStages), (j / kBStages) & 1))) break;
-          if (j > 0 && !(ok = Q ? wait(dp_done, (j - 1) & 1) : wait(acc_done(j - 1), ((j - 1) / kAStages) & 1))) break;
+          if (j > 0 && !(ok = kThree ? wait(dp_done, (j - 1) & 1) : wait(acc_done(j - 1), ((j - 1) / kAStages) & 1)))
+            break;
           tc_fence_after();
           product(col_dp(j), L::kFixB, ring_b(j));
           tc_commit(dp_full);
@@ -649,9 +655,8 @@ __device__ __forceinline__ void run_role(const CUtensorMap* tmFixA, const CUtens
       warp_arrive(dp_done, lane);
       if (!(ok = warp_wait_seen(a_seen, a_full(sa_next), a_phase_next, abort_flag, p.status))) break;
       const int valid_next = *static_cast<volatile int*>(&ctl.info[sa_next]);
-      if (Q)
-        s_seen = mbar_test_wait(s_full(j + 1), ((j + 1) >> 1) & 1);
-      else
+      if (kThree) s_seen = mbar_test_wait(s_full(j + 1), ((j + 1) >> 1) & 1);
+      if (!Q)
         rows_seen = mbar_test_wait(b_full((j + 1) % kBStages), ((j + 1) / kBStages) & 1);
       if (valid < kT) {
 #pragma unroll

@@ -501,3 +501,42 @@ def test_other_streams(ssa):
         assert all(same(a, b) for a, b in zip(c2, codes))
         del junk
     ssa.check_device()
+
+
+def test_offsets_past_32_bits(ssa):
+    """2.3 G elements per tensor: the last rows are right, through every kernel."""
+    from block_sparse_flashattention_ssa_b200 import positions as pos
+
+    T, H, D, n = 70_000, 256, 128, 200
+    lo = T - n
+    small = make([n], H, H, D, seed=30)
+    big = [torch.empty(T, H, D, dtype=torch.bfloat16, device="cuda") for _ in range(4)]
+    for b, t in zip(big, small[:4]):
+        b[lo:] = t
+    cu = torch.tensor([lo, T], dtype=torch.int32, device="cuda")
+    q, k, v, dout = big
+    out, lse = ssa.fwd_lse(q, k, v, cu, n)
+    grads = ssa.bwd(dout, q, k, v, out, lse, cu, n)
+    want_out, want_lse = ssa.fwd_lse(*small[:3], small[4], n)
+    want = ssa.bwd(small[3], *small[:3], want_out, want_lse, small[4], n)
+    assert same(out[lo:].contiguous(), want_out) and same(lse[:, lo:].contiguous(), want_lse)
+    assert all(same(g[lo:].contiguous(), w) for g, w in zip(grads, want))
+    del grads, out, lse, want, want_out, want_lse
+    codes, scales = ssa.save_fp8(q)
+    back = ssa.restore_fp8(codes, scales)
+    # blocks of 128 tokens count from the first one: compare whole blocks at the end
+    first = T // 128 * 128
+    c2, s2 = ssa.save_fp8(q[first:])
+    assert same(codes[first:].contiguous(), c2) and same(scales[-1:].contiguous(), s2)
+    assert same(back[first:].contiguous(), ssa.restore_fp8(c2, s2))
+    del codes, scales, back
+    p = torch.arange(T, dtype=torch.int32, device="cuda")
+    f, _ = pos.frequencies((D // 2,), device="cuda")
+    for interleaved in (False, True):
+        a = ssa.rotary(q, None, p, f, None, interleaved)[0]
+        b = ssa.rotary(q[lo:], None, p[lo:].contiguous(), f, None, interleaved)[0]
+        assert same(a[lo:].contiguous(), b)
+        del a
+    odd = ssa.rotary(q, None, p, f[:63].contiguous())[0]
+    assert same(odd[lo:].contiguous(), ssa.rotary(q[lo:], None, p[lo:].contiguous(), f[:63].contiguous())[0])
+    ssa.check_device()

@@ -175,6 +175,62 @@ def test_rows_checks(ssa):
         ssa._rows(None, "t", cpu, 5, 8)
 
 
+def test_calls_run_on_their_tensors_device_and_given_stream(ssa, monkeypatch):
+    """_run with stand-ins for two devices: the tensors' device is made current,
+    the given stream is used, and tensors are kept for it; a stream of another
+    device is refused."""
+    import contextlib
+
+    class Stream:
+        def __init__(self, device, handle):
+            self.device, self.cuda_stream = torch.device("cuda", device), handle
+
+        def __eq__(self, other):
+            return self.cuda_stream == other.cuda_stream
+
+        def __ne__(self, other):
+            return not self == other
+
+    class Tensor:
+        def __init__(self):
+            self.kept = []
+
+        def record_stream(self, s):
+            self.kept.append(s.cuda_stream)
+
+    log = []
+    current = {0: Stream(0, 100), 1: Stream(1, 200)}
+
+    @contextlib.contextmanager
+    def enter(what, value):
+        log.append((what, value))
+        yield
+
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda dev=None: current[0 if dev is None else dev.index])
+    monkeypatch.setattr(torch.cuda, "device", lambda d: enter("device", d.index))
+    monkeypatch.setattr(torch.cuda, "stream", lambda s: enter("stream", s.cuda_stream))
+    monkeypatch.setattr(ssa, "_current_handle", lambda t, dev: current[dev.index].cuda_stream)
+    made = Tensor()
+    body = lambda h: log.append(("run", h)) or (made,)
+    x = Tensor()
+
+    def run(dev, stream=None):
+        log.clear()
+        ssa._run(torch.device("cuda", dev), stream, (x, None), body)
+        return list(log)
+
+    assert run(0) == [("run", 100)]
+    assert run(1) == [("device", 1), ("stream", 200), ("run", 200)]  # another device than the current one
+    assert x.kept == [] and made.kept == []
+    assert run(0, Stream(0, 101)) == [("device", 0), ("stream", 101), ("run", 101)]
+    assert x.kept == [101] and made.kept == [100]
+    assert run(1, Stream(1, 201)) == [("device", 1), ("stream", 201), ("run", 201)]
+    assert made.kept == [100, 200]
+    with pytest.raises(ValueError, match="stream is on"):
+        run(0, Stream(1, 201))
+
+
 def test_position_tables(ssa):
     from block_sparse_flashattention_ssa_b200 import positions as pos
 

@@ -361,24 +361,31 @@ def _at(t):
     return None if t is None else t.data_ptr()
 
 
-def _is(t, dtype, dev, shape):
-    """The checks of _require() that pass in a correct call, in few steps: the
-    calls of a training step are short on the GPU for small batches."""
-    return t.dtype is dtype and t.device == dev and t.shape == shape and t.is_contiguous()
+def _all_are(dev, wanted) -> bool:
+    """Whether every (tensor, name, dtype, shape) passes _require(), in few
+    steps: the calls of a training step are short on the GPU for small batches."""
+    index = dev.index
+    try:
+        for t, _, dtype, shape in wanted:
+            if t.dtype is not dtype or t.shape != shape or t.get_device() != index or not t.is_contiguous():
+                return False
+    except AttributeError:
+        return False
+    return True
 
 
-def _need(t, name, dtype, dev, shape):
-    """_require() of an argument that must be there."""
-    import torch
+def _need(dev, wanted):
+    """_require() of the arguments that must be there."""
+    if not _all_are(dev, wanted):
+        for t, name, dtype, shape in wanted:
+            _require(t, name, dtype, dev, shape)
 
-    if not (isinstance(t, torch.Tensor) and _is(t, dtype, dev, shape)):
-        _require(t, name, dtype, dev, shape)
 
-
-def _may(t, name, dtype, dev, shape):
-    """_require() of an optional output."""
-    if t is not None:
-        _need(t, name, dtype, dev, shape)
+def _may(dev, wanted):
+    """_require() of the optional outputs among ``wanted``."""
+    given = [w for w in wanted if w[0] is not None]
+    if given:
+        _need(dev, given)
 
 
 def _current_handle(torch, dev):
@@ -430,23 +437,23 @@ def _no_overlap(outputs, inputs):
                 raise ValueError(f"{name} overlaps {other[2]}")
 
 
-def _check_shared_heads(q, k, v, cu_seqlens, qkv_dtype):
+def _check_shared_heads(torch, q, k, v, cu_seqlens, qkv_dtype):
     """Checks of fwd_lse and the backward passes: K and V may have fewer heads."""
-    import torch
-
     if not (isinstance(q, torch.Tensor) and q.is_cuda):
         raise ValueError("q must be a CUDA tensor")
     total, H, D = _shape(q)
     dev = q.device
-    _need(q, "q", qkv_dtype, dev, q.shape)
-    _require(k, "k", qkv_dtype, dev)
-    if k.dim() != 3 or k.shape[0] != total or k.shape[2] != D or k.shape[1] < 1 or H % k.shape[1] != 0:
-        raise ValueError(f"k has shape {tuple(k.shape)}, expected [{total}, a divisor of {H}, {D}]")
-    _need(v, "v", qkv_dtype, dev, k.shape)
-    _require(cu_seqlens, "cu_seqlens", torch.int32, dev)
-    if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2:
+    for t, name in ((k, "k"), (cu_seqlens, "cu_seqlens")):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor")
+    k_shape, cu_shape = k.shape, cu_seqlens.shape
+    _need(dev, ((q, "q", qkv_dtype, q.shape), (k, "k", qkv_dtype, k_shape), (v, "v", qkv_dtype, k_shape),
+                (cu_seqlens, "cu_seqlens", torch.int32, cu_shape)))
+    if len(k_shape) != 3 or k_shape[0] != total or k_shape[2] != D or k_shape[1] < 1 or H % k_shape[1] != 0:
+        raise ValueError(f"k has shape {tuple(k_shape)}, expected [{total}, a divisor of {H}, {D}]")
+    if len(cu_shape) != 1 or cu_shape[0] < 2:
         raise ValueError("cu_seqlens must be a 1-D tensor of batch + 1 offsets")
-    return dev, total, H, k.shape[1], D, cu_seqlens.numel() - 1
+    return dev, total, H, k_shape[1], D, cu_shape[0] - 1
 
 
 def fwd_lse(q, k, v, cu_seqlens, max_seqlen: int, threshold_scale_factor: float = 0.0, softmax_scale: float = 0.0,
@@ -459,9 +466,8 @@ def fwd_lse(q, k, v, cu_seqlens, max_seqlen: int, threshold_scale_factor: float 
     (as in fwd) to keep the decisions for bwd()."""
     import torch
 
-    dev, total, H, Hkv, D, batch = _check_shared_heads(q, k, v, cu_seqlens, torch.bfloat16)
-    _may(out, "out", torch.bfloat16, dev, q.shape)
-    _may(lse, "lse", torch.float32, dev, (H, total))
+    dev, total, H, Hkv, D, batch = _check_shared_heads(torch, q, k, v, cu_seqlens, torch.bfloat16)
+    _may(dev, ((out, "out", torch.bfloat16, q.shape), (lse, "lse", torch.float32, (H, total))))
     nq = -1
     if skip_counter is not None or decision_bitmap is not None:
         nq = _per_unit_qblocks(dev, H, total, batch, _forward_outputs(skip_counter, decision_bitmap, None, max_seqlen))
@@ -485,24 +491,22 @@ def _backward(what, dout, q, k, v, extra, out, lse, cu_seqlens, max_seqlen, soft
               workspace, stream, qkv_dtype, workspace_bytes, call):
     import torch
 
-    dev, total, H, Hkv, D, batch = _check_shared_heads(q, k, v, cu_seqlens, qkv_dtype)
-    bf16 = torch.bfloat16
-    _need(dout, "dout", bf16, dev, q.shape)
-    _need(out, "out", bf16, dev, q.shape)
-    _need(lse, "lse", torch.float32, dev, (H, total))
-    _may(dq, "dq", bf16, dev, q.shape)
-    _may(dk, "dk", bf16, dev, k.shape)
-    _may(dv, "dv", bf16, dev, k.shape)
-    _require(workspace, "workspace", None, dev, allow_none=True)
-    for t, name, heads in extra:
-        _need(t, name, torch.float32, dev, ((total + TILE - 1) // TILE, heads))
+    dev, total, H, Hkv, D, batch = _check_shared_heads(torch, q, k, v, cu_seqlens, qkv_dtype)
+    bf16, q_shape, k_shape = torch.bfloat16, q.shape, k.shape
+    _need(dev, ((dout, "dout", bf16, q_shape), (out, "out", bf16, q_shape), (lse, "lse", torch.float32, (H, total)))
+          + tuple((t, name, torch.float32, ((total + TILE - 1) // TILE, heads)) for t, name, heads in extra))
+    _may(dev, ((dq, "dq", bf16, q_shape), (dk, "dk", bf16, k_shape), (dv, "dv", bf16, k_shape)))
+    if workspace is not None:
+        _require(workspace, "workspace", None, dev)
     nq, max_seqlen = -1, int(max_seqlen)
     if decision_bitmap is not None:
         nq = _per_unit_qblocks(dev, H, total, batch, [(decision_bitmap, "decision_bitmap", (torch.int32, torch.uint32),
                                                         (bitmap_words(max_seqlen),))])
-    _no_overlap([(dq, "dq"), (dk, "dk"), (dv, "dv"), (workspace, "workspace")],
-                [(dout, "dout"), (q, "q"), (k, "k"), (v, "v"), (out, "out"), (lse, "lse"), (cu_seqlens, "cu_seqlens"),
-                 (decision_bitmap, "decision_bitmap")] + [(t, name) for t, name, _ in extra])
+    if not (dq is None and dk is None and dv is None and workspace is None):
+        _no_overlap([(dq, "dq"), (dk, "dk"), (dv, "dv"), (workspace, "workspace")],
+                    [(dout, "dout"), (q, "q"), (k, "k"), (v, "v"), (out, "out"), (lse, "lse"),
+                     (cu_seqlens, "cu_seqlens"), (decision_bitmap, "decision_bitmap")]
+                    + [(t, name) for t, name, _ in extra])
     need = workspace_bytes(total, batch, H, Hkv, D)
     if need < 0:
         raise SSAError(int(need), what)
@@ -582,9 +586,8 @@ def save_fp8(x, codes=None, scales=None, stream=None):
         raise ValueError("x must be a CUDA tensor")
     total, H, D = _shape(x)
     dev, s_shape = x.device, ((total + TILE - 1) // TILE, H)
-    _need(x, "x", torch.bfloat16, dev, x.shape)
-    _may(codes, "codes", torch.uint8, dev, x.shape)
-    _may(scales, "scales", torch.float32, dev, s_shape)
+    _need(dev, ((x, "x", torch.bfloat16, x.shape),))
+    _may(dev, ((codes, "codes", torch.uint8, x.shape), (scales, "scales", torch.float32, s_shape)))
     _no_overlap([(codes, "codes"), (scales, "scales")], [(x, "x")])
 
     def body(handle):
@@ -604,9 +607,9 @@ def restore_fp8(codes, scales, out=None, stream=None):
         raise ValueError("codes must be a CUDA tensor")
     total, H, D = _shape(codes)
     dev = codes.device
-    _need(codes, "codes", torch.uint8, dev, codes.shape)
-    _need(scales, "scales", torch.float32, dev, ((total + TILE - 1) // TILE, H))
-    _may(out, "out", torch.bfloat16, dev, codes.shape)
+    _need(dev, ((codes, "codes", torch.uint8, codes.shape),
+                (scales, "scales", torch.float32, ((total + TILE - 1) // TILE, H))))
+    _may(dev, ((out, "out", torch.bfloat16, codes.shape),))
     _no_overlap([(out, "out")], [(codes, "codes"), (scales, "scales")])
 
     def body(handle):
@@ -694,13 +697,13 @@ def rotary(q, k, positions, inv_freq, sections=None, interleaved: bool = False, 
         raise ValueError("q must be a CUDA tensor")
     total, H, D = _shape(q)
     dev = q.device
-    if not (isinstance(positions, torch.Tensor) and _is(positions, torch.int32, dev, positions.shape)):
-        _require(positions, "positions", torch.int32, dev)
+    for t, name in ((positions, "positions"), (inv_freq, "inv_freq")):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor")
+    _need(dev, ((positions, "positions", torch.int32, positions.shape), (inv_freq, "inv_freq", torch.float64, inv_freq.shape)))
     axes = 1 if positions.dim() == 1 else positions.shape[-1]
     if positions.shape != ((total,) if positions.dim() == 1 else (total, axes)):
         raise ValueError(f"positions has shape {tuple(positions.shape)}, expected [{total}] or [{total}, axes]")
-    if not (isinstance(inv_freq, torch.Tensor) and _is(inv_freq, torch.float64, dev, inv_freq.shape)):
-        _require(inv_freq, "inv_freq", torch.float64, dev)
     pairs = inv_freq.numel()
     if inv_freq.dim() != 1 or 2 * pairs > D:
         raise ValueError(f"inv_freq must be 1-D with at most {D // 2} frequencies")

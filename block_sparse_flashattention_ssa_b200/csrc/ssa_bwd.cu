@@ -252,6 +252,12 @@ __device__ void locate(const Params& p, int x, int lane, bool report, Unit& u) {
   }
 }
 
+// A small main kernel is launched while rows_kernel still runs (programmatic
+// dependent launch, see launch()) and waits for it only where it reads the row
+// values: its prologue, first loads and S overlap with it.
+__device__ __forceinline__ void next_kernel_may_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_for_rows() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // -D_r = -dO_r.O_r and -L_r log2 e of one query block and head; D / 8 lanes per
 // row, 16 bytes of dO and O each. Bound by the read of dO and O. The one row of
 // a sequence of length one gets dP - D = dO.(v - O) in place of -D: the forward
@@ -260,6 +266,7 @@ __device__ void locate(const Params& p, int x, int lane, bool report, Unit& u) {
 template <int D>
 __global__ void __launch_bounds__(256) rows_kernel(const __grid_constant__ Params p) {
   __shared__ Unit u;
+  next_kernel_may_start();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, head = blockIdx.y;
   if (warp == 0) locate(p, static_cast<int>(blockIdx.x), lane, blockIdx.x == 0 && head == 0, u);
   __syncthreads();
@@ -420,6 +427,7 @@ __device__ __forceinline__ void run_role(const CUtensorMap* tmFixA, const CUtens
                     u.start + u.block * kT);
       }
     }
+    if (!Q) wait_for_rows();  // the ring brings the row values as well
     const int ring_heads = Q ? 1 : group;
     const int chunks = (nt + 31) / 32;
     // Bits of the tiles base .. base+31 that this CTA's block skips.
@@ -588,6 +596,7 @@ __device__ __forceinline__ void run_role(const CUtensorMap* tmFixA, const CUtens
     if (Q) {
       key_mean<D>(p, u, head / group, warp - kEwWarp, lane, mean_key);
       named_barrier_sync(1, kEwThreads);
+      wait_for_rows();
       const float* r = p.rows + (static_cast<int64_t>(head) * p.units + u.gqb0 + u.block) * (2 * kT);
       row_bias = r[row];
       row_ndelta = r[kT + row];
@@ -899,13 +908,20 @@ int launch(Params p, const void* q, const void* k, const void* v, cudaStream_t s
   config.blockDim = dim3(kThreads);
   config.dynamicSmemBytes = smem;
   config.stream = stream;
-  cudaLaunchAttribute cluster{};
-  cluster.id = cudaLaunchAttributeClusterDimension;
-  cluster.val.clusterDim.x = 1;
-  cluster.val.clusterDim.y = static_cast<unsigned>(split);
-  cluster.val.clusterDim.z = 1;
-  config.attrs = &cluster;
-  config.numAttrs = split > 1 ? 1 : 0;
+  // An early start gains 3 to 5 us in batches that leave SMs free or are split
+  // (128 x 1 x 128 16.5 / 12.8 us, 512 x 4 20.9 / 16.9), and costs as much when
+  // long unsplit walks take nearly every SM (1000 x 8 28.3 / 31.3, 1700 x 5 39.5 /
+  // 47.3): a CTA takes a whole SM, and those that find rows_kernel on theirs wait.
+  const bool early = split > 1 || 2 * static_cast<int64_t>(config.gridDim.x) * config.gridDim.y <= kSMs;
+  cudaLaunchAttribute attrs[2]{};
+  attrs[0].id = cudaLaunchAttributeClusterDimension;
+  attrs[0].val.clusterDim.x = 1;
+  attrs[0].val.clusterDim.y = static_cast<unsigned>(split);
+  attrs[0].val.clusterDim.z = 1;
+  attrs[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attrs[1].val.programmaticStreamSerializationAllowed = early ? 1 : 0;
+  config.attrs = attrs;
+  config.numAttrs = early ? 2 : 0;  // neither split nor early: a plain launch
   e = cudaLaunchKernelEx(&config, bwd_kernel<D>, tq, tk, tv, tdo, p);
   return e == cudaSuccess ? SSA_OK : internal::fail(e);
 }

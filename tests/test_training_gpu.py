@@ -540,3 +540,52 @@ def test_offsets_past_32_bits(ssa):
     odd = ssa.rotary(q, None, p, f[:63].contiguous())[0]
     assert same(odd[lo:].contiguous(), ssa.rotary(q[lo:], None, p[lo:].contiguous(), f[:63].contiguous())[0])
     ssa.check_device()
+
+
+def test_refusals(ssa):
+    """Every argument is checked before a launch: types, shapes, devices,
+    contiguity, alignment, overlaps, sizes."""
+    lens, H, Hk, D = [200], 4, 2, 64
+    q, k, v, dout, cu = make(lens, H, Hk, D, seed=31)
+    out, lse = ssa.fwd_lse(q, k, v, cu, 200)
+    bm = bitmap_for(ssa, lens, H)
+    codes = [ssa.save_fp8(t) for t in (q, k, v)]
+    p, f = torch.arange(200, dtype=torch.int32, device="cuda"), torch.ones(32, dtype=torch.float64, device="cuda")
+    flat = torch.empty(q.numel() + 8, dtype=torch.bfloat16, device="cuda")
+    crooked = flat[4:4 + q.numel()].view(q.shape)  # 8 bytes off a 16-byte boundary
+    fwd = lambda q=q, k=k, v=v, cu=cu, **kw: ssa.fwd_lse(q, k, v, cu, 200, **kw)
+    bwd = lambda dout=dout, q=q, k=k, v=v, out=out, lse=lse, cu=cu, **kw: ssa.bwd(dout, q, k, v, out, lse, cu, 200, **kw)
+    bad = [
+        lambda: fwd(q=q.cpu()), lambda: fwd(k=k.cpu()), lambda: fwd(q=q.float()), lambda: fwd(q=q[:, :, ::2]), lambda: fwd(q=q[0]),
+        lambda: fwd(k=k[:, :1].contiguous(), v=v), lambda: fwd(k=k[:100], v=v[:100]), lambda: fwd(k=torch.cat([k, k[:, :1]], 1), v=v),
+        lambda: fwd(cu=cu.long()), lambda: fwd(cu=cu[:1]), lambda: fwd(cu=cu.cpu()), lambda: fwd(out=out.float()), lambda: fwd(out=q),
+        lambda: fwd(lse=lse[:, :100]), lambda: fwd(lse=lse.double()), lambda: fwd(decision_bitmap=bm[:, :, :0]), lambda: fwd(k=None),
+        lambda: bwd(dout=dout[:100]), lambda: bwd(dout=None), lambda: bwd(out=out.float()), lambda: bwd(lse=lse.T), lambda: bwd(dq=q),
+        lambda: bwd(dq=dout), lambda: bwd(dk=torch.empty_like(q)), lambda: bwd(dk=v), lambda: bwd(dq=out, dk=None),
+        lambda: bwd(workspace=q.view(-1)), lambda: bwd(workspace=flat.cpu()), lambda: bwd(decision_bitmap=bm.float()),
+        lambda: bwd(decision_bitmap=bm[:3]), lambda: bwd(k=k.transpose(0, 1)),
+        lambda: ssa.bwd_fp8(dout, (codes[0][0], codes[1][1]), codes[1], codes[2], out, lse, cu, 200),
+        lambda: ssa.bwd_fp8(dout, (q, codes[0][1]), codes[1], codes[2], out, lse, cu, 200),
+        lambda: ssa.save_fp8(q.float()), lambda: ssa.save_fp8(q[0]), lambda: ssa.save_fp8(q, codes=q.view(torch.uint8)[..., :64]),
+        lambda: ssa.save_fp8(q, scales=codes[1][1]), lambda: ssa.restore_fp8(q, codes[0][1]), lambda: ssa.restore_fp8(codes[0][0], codes[1][1]),
+        lambda: ssa.rotary(q, k, p[:100], f), lambda: ssa.rotary(q, k, p.long(), f), lambda: ssa.rotary(q, k, p, f.float()),
+        lambda: ssa.rotary(q, k, p, f.repeat(2)), lambda: ssa.rotary(q, k[:100], p, f), lambda: ssa.rotary(q, k, p, f, sections=(31,)),
+        lambda: ssa.rotary(q, k, p[:, None].repeat(1, 2), f), lambda: ssa.rotary(q, k, p, f, out_q=k), lambda: ssa.rotary(q, k, p, f, out_k=q),
+        lambda: ssa.rotary(q, None, p, f, out_k=k), lambda: ssa.rotary(q, q, p, f, out_q=q, out_k=q), lambda: ssa.rotary(q[:, ::2], None, p, f),
+        lambda: ssa.rotary(q[..., :32], None, p, f[:16]),
+    ]
+    for i, call in enumerate(bad):
+        with pytest.raises((ValueError, TypeError)):
+            call()
+            pytest.fail(f"call {i} was accepted")
+    refused = [
+        lambda: fwd(q=crooked), lambda: bwd(dout=crooked), lambda: bwd(dq=crooked), lambda: ssa.save_fp8(crooked),
+        lambda: bwd(workspace=torch.empty(1024, dtype=torch.uint8, device="cuda")), lambda: fwd(softmax_scale=math.nan),
+        lambda: fwd(threshold_scale_factor=math.inf), lambda: ssa.save_fp8(q.view(200, 2, 128)[:, :, :96].contiguous()),
+        lambda: ssa.rotary(q, k, p, f, scale=math.inf),
+    ]
+    for i, call in enumerate(refused):
+        with pytest.raises(ssa.SSAError):
+            call()
+            pytest.fail(f"call {i} was accepted")
+    ssa.check_device()

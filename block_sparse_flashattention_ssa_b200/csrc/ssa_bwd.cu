@@ -256,7 +256,10 @@ __device__ void locate(const Params& p, int x, int lane, bool report, Unit& u) {
 // dependent launch, see launch()) and waits for it only where it reads the row
 // values: its prologue, first loads and S overlap with it.
 __device__ __forceinline__ void next_kernel_may_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-__device__ __forceinline__ void wait_for_rows() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void wait_for_rows() {
+  // The fence: the kv role reads the row values by bulk copies.
+  asm volatile("griddepcontrol.wait;\n fence.proxy.async.global;" ::: "memory");
+}
 
 // -D_r = -dO_r.O_r and -L_r log2 e of one query block and head; D / 8 lanes per
 // row, 16 bytes of dO and O each. Bound by the read of dO and O. The one row of

@@ -487,6 +487,16 @@ def fwd_lse(q, k, v, cu_seqlens, max_seqlen: int, threshold_scale_factor: float 
     return _run(dev, stream, (q, k, v, cu_seqlens, out, lse, skip_counter, decision_bitmap), body)
 
 
+@functools.lru_cache(maxsize=256)
+def _bwd_workspace(total, batch, H, Hkv, D):
+    return _lib.ssa_bwd_workspace_bytes(total, batch, H)
+
+
+@functools.lru_cache(maxsize=256)
+def _bwd_fp8_workspace(total, batch, H, Hkv, D):
+    return _lib.ssa_bwd_fp8_workspace_bytes(total, batch, H, Hkv, D)
+
+
 def _backward(what, dout, q, k, v, extra, out, lse, cu_seqlens, max_seqlen, softmax_scale, decision_bitmap, dq, dk, dv,
               workspace, stream, qkv_dtype, workspace_bytes, call):
     import torch
@@ -539,7 +549,7 @@ def bwd(dout, q, k, v, out, lse, cu_seqlens, max_seqlen: int, softmax_scale: flo
 
     return _backward(
         "ssa_bwd", dout, q, k, v, [], out, lse, cu_seqlens, max_seqlen, softmax_scale, decision_bitmap, dq, dk, dv,
-        workspace, stream, torch.bfloat16, lambda total, batch, H, Hkv, D: _lib.ssa_bwd_workspace_bytes(total, batch, H),
+        workspace, stream, torch.bfloat16, _bwd_workspace,
         lambda g, *rest: _lib.ssa_bwd(g, _at(q), _at(k), _at(v), *rest))
 
 
@@ -554,7 +564,7 @@ def bwd_fp8(dout, q_saved, k_saved, v_saved, out, lse, cu_seqlens, max_seqlen: i
     return _backward(
         "ssa_bwd_fp8", dout, q, k, v, [(qs, "q_scales", heads(q)), (ks, "k_scales", heads(k)), (vs, "v_scales", heads(v))],
         out, lse, cu_seqlens, max_seqlen, softmax_scale, decision_bitmap, dq, dk, dv, workspace, stream, torch.uint8,
-        _lib.ssa_bwd_fp8_workspace_bytes,
+        _bwd_fp8_workspace,
         lambda g, *rest: _lib.ssa_bwd_fp8(g, _at(q), _at(qs), _at(k), _at(ks), _at(v), _at(vs), *rest))
 
 

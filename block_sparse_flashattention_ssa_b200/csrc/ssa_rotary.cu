@@ -38,6 +38,7 @@ struct Params {
   int tokens, axes, dim, rot;
   int axis_end[kMaxAxes];  // pairs before axis_end[a] (and from axis_end[a - 1]) turn with axis a
   float scale, sign;
+  bool copies;  // false when every output is its input: the elements past the rotated part stay where they are
 };
 
 __device__ __forceinline__ void turn_pair(float a, float b, float2 cs, float& lo, float& hi) {
@@ -130,7 +131,7 @@ __global__ void __launch_bounds__(kThreads, 4) rotary_kernel(const __grid_consta
   __syncthreads();
 
   const int first_copied = INTERLEAVED && N == 8 ? turned * 8 : p.rot;
-  const int pieces = turned + (p.dim - first_copied) / kCopied;  // at most 256
+  const int pieces = turned + (p.copies ? (p.dim - first_copied) / kCopied : 0);  // 1 to 256
   const int stride = kThreads / pieces;                          // rows the CTA takes at once
   const int piece = static_cast<int>(threadIdx.x) % pieces;
   int row = static_cast<int>(threadIdx.x) / pieces;
@@ -350,6 +351,7 @@ extern "C" int ssa_rotary(const void* q, const void* k, void* q_out, void* k_out
   // Largest run of elements, up to 8, that suits every address and stride and,
   // in the half layout, the distance between the elements of a pair.
   uint64_t aligned = 0;
+  p.copies = false;
   for (int i = 0; i < n; ++i) {
     const uintptr_t both = reinterpret_cast<uintptr_t>(in[i]) | reinterpret_cast<uintptr_t>(out[i]);
     if (both & 1u) return SSA_ERR_UNSUPPORTED;
@@ -359,6 +361,7 @@ extern "C" int ssa_rotary(const void* q, const void* k, void* q_out, void* k_out
     p.xs[i] = xs[i];
     p.ys[i] = ys[i];
     p.heads[i] = i ? num_kv_heads : num_heads;
+    if (in[i] != out[i] || (xs[i] != ys[i] && total_tokens > 1)) p.copies = true;
   }
   uint64_t steps = 8 | aligned | (interleaved ? 0 : static_cast<uint64_t>(rotary_dim / 2));
   steps &= ~steps + 1;  // its lowest set bit
@@ -366,6 +369,7 @@ extern "C" int ssa_rotary(const void* q, const void* k, void* q_out, void* k_out
                                                 n == 2 ? k : nullptr, n == 2 ? k_out : nullptr});
       rc != SSA_OK)
     return rc;
+  if (rotary_dim == 0 && !p.copies) return SSA_OK;
   p.positions = positions;
   p.inv_freq = inv_freq;
   p.tokens = total_tokens;

@@ -356,7 +356,7 @@ def test_rotary(ssa, T, H, Hk, D, rot, axes, interleaved, transpose):
 
 
 @pytest.mark.parametrize("interleaved", [False, True])
-@pytest.mark.parametrize("rot", [64, 62, 60])
+@pytest.mark.parametrize("rot", [64, 62, 60, 36, 32, 30, 0])
 def test_rotary_slices_in_place_and_alone(ssa, interleaved, rot):
     """Q and K as slices of a fused projection, written in place, and Q alone."""
     from block_sparse_flashattention_ssa_b200 import positions as pos

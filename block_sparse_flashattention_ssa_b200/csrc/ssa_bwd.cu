@@ -814,7 +814,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int y = static_cast<int>(blockIdx.y);
   if (warp == 0) locate(p, static_cast<int>(blockIdx.x), lane, blockIdx.x == 0 && y == 0, ctl.u);
   __syncthreads();
-  if (ctl.u.seq < 0) return;  // uniform
+  if (ctl.u.seq < 0) {  // uniform
+    if (threadIdx.x == 0) wait_for_rows();  // no CTA, and so not this kernel, ends before rows_kernel has
+    return;
+  }
 
   if (threadIdx.x == 0) {
     mbar_init(smem_u32(&ctl.fix_full), 1);

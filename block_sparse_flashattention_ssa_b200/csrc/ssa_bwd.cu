@@ -200,7 +200,22 @@ __device__ __forceinline__ void warp_arrive(uint32_t bar, int lane) {
 // bitmap was sized for), which is reported in the status word. Up to 32
 // sequences are numbered longest first, so the longest walks start first;
 // longer batches keep their order. Units are indexed in sequence order.
+//
+// A CTA runs this and the other code outside its walk once, on a cold
+// instruction cache: short code (one sequence apart, loops left rolled) takes
+// 1000 cycles here where unrolled code took 3800.
 __device__ void locate(const Params& p, int x, int lane, bool report, Unit& u) {
+  if (p.batch == 1) {
+    if (lane == 0) {
+      const int lo = p.cu_seqlens[0], hi = p.cu_seqlens[1], len = hi - lo;
+      const bool in = lo >= 0 && len >= 0 && hi <= p.total_tokens;
+      const int nq = in ? (len + kT - 1) / kT : 0;
+      const bool bad = !in || (p.bitmap && nq > p.max_tiles) || (p.nq_check >= 0 && nq != p.nq_check);
+      if (bad && report) atomicOr(p.status, kStatusDeviceArg);
+      u = Unit{!bad && x < nq ? 0 : -1, x, len, lo, 0, nq};
+    }
+    return;
+  }
   int seq = -1, block = 0, S = 0, start = 0, gqb0 = 0, bad = 0, total = 0, seen = 0;
   for (int base = 0; base < p.batch; base += 32) {
     const int b = base + lane;
@@ -214,7 +229,7 @@ __device__ void locate(const Params& p, int x, int lane, bool report, Unit& u) {
       if (p.bitmap && nq > p.max_tiles) bad = 1;
     }
     int off = nq;  // inclusive prefix sum in sequence order
-#pragma unroll
+#pragma unroll 1
     for (int o = 1; o < 32; o <<= 1) {
       const int t = __shfl_up_sync(kFull, off, o);
       if (lane >= o) off += t;
@@ -224,6 +239,7 @@ __device__ void locate(const Params& p, int x, int lane, bool report, Unit& u) {
     int first = seen + off;  // number of this sequence's first block in the order of work
     if (p.batch <= 32) {
       first = 0;
+#pragma unroll 1
       for (int o = 0; o < p.batch; ++o) {
         const int len_o = __shfl_sync(kFull, len, o), nq_o = __shfl_sync(kFull, nq, o);
         if (len_o > len || (len_o == len && o < b)) first += nq_o;
@@ -328,40 +344,48 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
       : "memory");
 }
 
-// Mean of the keys of this block's rows, finite values only (the dQ of a row
-// that saw others is not finite anyway); eight warps take D / 8 columns each.
+// Mean key of this block: of 32 of its rows, evenly spread (enough to hold what
+// the keys have in common), finite values only (the dQ of a row that saw others
+// is not finite anyway). Eight warps take D / 8 columns each; one row per lane.
 template <int D>
 __device__ __forceinline__ void key_mean(const Params& p, const Unit& u, int head, int warp, int lane, float* mean) {
   constexpr int kCols = D / 8;
   const int rows = min(kT, u.S - u.block * kT);
+  const int64_t token = u.start + u.block * kT + ((lane * rows) >> 5);
+  const uint4* k = reinterpret_cast<const uint4*>(p.k + (token * p.num_kv_heads + head) * D + warp * kCols);
   float sum[kCols];
 #pragma unroll
-  for (int i = 0; i < kCols; ++i) sum[i] = 0.f;
+  for (int i = 0; i < kCols / 8; ++i) {
+    const uint4 v = k[i];
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-  for (int n = 0; n < kT / 32; ++n) {
-    const int r = lane + n * 32;
-    if (r < rows) {
-      const __nv_bfloat16* k =
-          p.k + (static_cast<int64_t>(u.start + u.block * kT + r) * p.num_kv_heads + head) * D + warp * kCols;
-#pragma unroll
-      for (int i = 0; i < kCols / 8; ++i) {
-        const uint4 v = reinterpret_cast<const uint4*>(k)[i];
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const float2 f = unpack_bf16x2(w[c]);
-          sum[i * 8 + 2 * c] += isfinite(f.x) ? f.x : 0.f;
-          sum[i * 8 + 2 * c + 1] += isfinite(f.y) ? f.y : 0.f;
-        }
-      }
+    for (int c = 0; c < 4; ++c) {
+      const float2 f = unpack_bf16x2(w[c]);
+      sum[i * 8 + 2 * c] = isfinite(f.x) ? f.x : 0.f;
+      sum[i * 8 + 2 * c + 1] = isfinite(f.y) ? f.y : 0.f;
     }
   }
+  // Each step adds lanes o apart and leaves each of them half of the columns,
+  // until one is left; then the lanes that share it add up.
+  int column = 0;
 #pragma unroll
-  for (int i = 0; i < kCols; ++i) {
+  for (int step = 0; step < 5; ++step) {
+    const int o = 16 >> step, n = kCols >> (step + 1);  // constants, unrolled
+    const bool upper = (lane & o) != 0;
+    if (n > 0) {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum[i] += __shfl_xor_sync(kFull, sum[i], o);
-    if (lane == 0) mean[warp * kCols + i] = sum[i] / static_cast<float>(rows);
+      for (int i = 0; i < kCols / 2; ++i) {
+        if (i < n) {
+          const float send = upper ? sum[i] : sum[n + i], keep = upper ? sum[n + i] : sum[i];
+          sum[i] = keep + __shfl_xor_sync(kFull, send, o);
+        }
+      }
+      column += upper ? n : 0;
+    } else {
+      sum[0] += __shfl_xor_sync(kFull, sum[0], o);
+    }
   }
+  mean[warp * kCols + column] = sum[0] * (1.f / 32.f);  // lanes with the same column hold the same sum
 }
 
 // All threads of the cluster; orders shared-memory accesses before it against
@@ -389,8 +413,9 @@ __device__ __forceinline__ void run_role(const CUtensorMap* tmFixA, const CUtens
   constexpr int kAccs = Q ? 1 : 2;
   constexpr bool kThree = Q || D == 64;           // three score regions; else two, which change places
   constexpr uint32_t kColAccB = kColAccA + D;     // kv role
-  constexpr int kPartRow = D + 4;  // floats; the pad spreads the rows over the banks
-  static_assert(2 * kT * kPartRow * 4 <= L::kRows, "a cluster's partial sums reuse the tiles' shared memory");
+  constexpr int kPartRow = D + 4;         // floats; the pad spreads the rows over the banks
+  constexpr int kStageRow = 2 * D + 16;  // bytes, likewise
+  static_assert(2 * kT * kPartRow * 4 <= L::kRows, "the results are staged in the tiles' shared memory");
   Ctl& ctl = *reinterpret_cast<Ctl*>(smem + L::kCtl);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const Unit u = ctl.u;
@@ -420,8 +445,6 @@ __device__ __forceinline__ void run_role(const CUtensorMap* tmFixA, const CUtens
     int it = 0, b_issued = 0;  // ring tiles issued
     bool ok = true;
     if (lane == 0) {
-      prefetch_tmap(tmRingA);
-      prefetch_tmap(tmRingB);
       mbar_arrive_expect_tx(fix_full, 2 * L::kTileBytes);
       for (int ch = 0; ch < L::kChunks; ++ch) {
         tma_load_3d(smem_u32(smem + L::kFixA + ch * L::kChunkBytes), tmFixA, fix_full, ch * 64, head,
@@ -591,7 +614,6 @@ __device__ __forceinline__ void run_role(const CUtensorMap* tmFixA, const CUtens
     const int half = (warp - kEwWarp) >> 2;  // columns [64 half, 64 half + 64)
     const int row = (warp & 3) * 32 + lane;
     const uint32_t lanes = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
-    const bool row_valid = u.block * kT + row < u.S;
     float row_bias = 0.f, row_ndelta = 0.f;  // q role: this thread's row
     const float2 zero = make_float2(0.f, 0.f);
     float2 exact[2] = {zero, zero}, rounded[2] = {zero, zero};  // q role: sums of its dS before and after rounding
@@ -721,13 +743,10 @@ __device__ __forceinline__ void run_role(const CUtensorMap* tmFixA, const CUtens
     if (ok) ok = warp_wait(acc_full, 0, abort_flag, p.status);
     if (ok) {
       tc_fence_after();
-      const int heads = Q ? p.num_heads : p.num_kv_heads;
-      const int64_t at = (static_cast<int64_t>(u.start + u.block * kT + row) * heads + head) * D + half * (D / 2);
-#pragma unroll
+#pragma unroll 1
       for (int a = 0; a < kAccs; ++a) {
-        __nv_bfloat16* dst = (Q ? p.dq : (a ? p.dv : p.dk)) + at;
         const float f = a ? 1.f : p.scale;
-#pragma unroll
+#pragma unroll 1
         for (int ch = 0; ch < D / 64; ++ch) {
           uint32_t o[32];
           tmem_ld_x32(lanes + (a ? kColAccB : kColAccA) + half * (D / 2) + ch * 32, o);
@@ -741,16 +760,34 @@ __device__ __forceinline__ void run_role(const CUtensorMap* tmFixA, const CUtens
             uint4* part = reinterpret_cast<uint4*>(smem + ((a * kT + row) * kPartRow + half * (D / 2) + ch * 32) * 4);
 #pragma unroll
             for (int i = 0; i < 8; ++i) part[i] = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
-          } else if (row_valid) {
+          } else {
+            uint4* part = reinterpret_cast<uint4*>(smem + (a * kT + row) * kStageRow + (half * (D / 2) + ch * 32) * 2);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               uint32_t w[4];
 #pragma unroll
               for (int k = 0; k < 4; ++k)
                 w[k] = pack_bf16x2(__uint_as_float(o[8 * i + 2 * k]) * f, __uint_as_float(o[8 * i + 2 * k + 1]) * f);
-              reinterpret_cast<uint4*>(dst + ch * 32)[i] = make_uint4(w[0], w[1], w[2], w[3]);
+              part[i] = make_uint4(w[0], w[1], w[2], w[3]);
             }
           }
+        }
+      }
+    }
+    if (split == 1) {  // whole rows of 128 or 256 bytes to memory, not 16 bytes of 32 rows at a time
+      named_barrier_sync(1, kEwThreads);  // every element-wise warp comes here, with or without an error
+      if (ok) {
+        const int heads = Q ? p.num_heads : p.num_kv_heads;
+        constexpr int kWords = D / 8;  // 16-byte words of a row
+        const int rows = min(kT, u.S - u.block * kT);
+        const int64_t base = (static_cast<int64_t>(u.start + u.block * kT) * heads + head) * D;
+#pragma unroll 1
+        for (int a = 0; a < kAccs; ++a) {
+          __nv_bfloat16* dst = (Q ? p.dq : (a ? p.dv : p.dk)) + base;
+#pragma unroll 4
+          for (int i = threadIdx.x - 32 * kEwWarp; i < rows * kWords; i += kEwThreads)
+            *reinterpret_cast<uint4*>(dst + static_cast<int64_t>(i / kWords) * heads * D + i % kWords * 8) =
+                *reinterpret_cast<const uint4*>(smem + (a * kT + i / kWords) * kStageRow + i % kWords * 16);
         }
       }
     }
@@ -812,14 +849,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   Ctl& ctl = *reinterpret_cast<Ctl*>(smem + L::kCtl);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int y = static_cast<int>(blockIdx.y);
-  if (warp == 0) locate(p, static_cast<int>(blockIdx.x), lane, blockIdx.x == 0 && y == 0, ctl.u);
-  __syncthreads();
-  if (ctl.u.seq < 0) {  // uniform
-    if (threadIdx.x == 0) wait_for_rows();  // no CTA, and so not this kernel, ends before rows_kernel has
-    return;
-  }
-
-  if (threadIdx.x == 0) {
+  if (warp == 0) {
+    locate(p, static_cast<int>(blockIdx.x), lane, blockIdx.x == 0 && y == 0, ctl.u);
+  } else if (warp == kSWarp) {
+    tmem_alloc(smem_u32(&ctl.tmem_base), kTmemCols);
+    tmem_relinquish();
+  } else if (warp == kDPWarp && lane == 0) {
     mbar_init(smem_u32(&ctl.fix_full), 1);
     for (int i = 0; i < kAStages; ++i) {
       mbar_init(smem_u32(&ctl.a_full[i]), 1);
@@ -840,14 +875,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < 3; ++i) mbar_init(smem_u32(&ctl.drain[i]), 1);
     ctl.abort_flag = 0;
     fence_mbar_init();
-  }
-  if (warp == kSWarp) {
-    tmem_alloc(smem_u32(&ctl.tmem_base), kTmemCols);
-    tmem_relinquish();
+  } else if (warp == kAccWarp && lane == 0) {
+    prefetch_tmap(&tmQ);
+    prefetch_tmap(&tmK);
+    prefetch_tmap(&tmV);
+    prefetch_tmap(&tmdO);
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  if (ctl.u.seq < 0) {  // uniform
+    if (threadIdx.x == 0) wait_for_rows();  // no CTA, and so not this kernel, ends before rows_kernel has
+    if (warp == kSWarp) tmem_dealloc(ctl.tmem_base, kTmemCols);
+    return;
+  }
 
   const int kv_ctas = p.num_kv_heads * p.split[0];
   if (y < kv_ctas)

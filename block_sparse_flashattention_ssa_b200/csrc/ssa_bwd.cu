@@ -741,6 +741,10 @@ __device__ __forceinline__ void run_role(const CUtensorMap* tmFixA, const CUtens
       excess = sums[row] + sums[kT + row];
     }
     if (ok) ok = warp_wait(acc_full, 0, abort_flag, p.status);
+    // Results are staged over the tiles: all loads must have landed. Where tiles
+    // were walked the accumulators say so; where none was, the fixed tiles may
+    // still be on their way.
+    if (ok && !any) ok = warp_wait(fix_full, 0, abort_flag, p.status);
     if (ok) {
       tc_fence_after();
 #pragma unroll 1

@@ -167,6 +167,25 @@ def test_bwd_more_than_32_tiles_and_a_sparse_map(ssa):
     assert not grads[0][3 * 128:4 * 128].any() and not grads[1][20 * 128:21 * 128].any()
 
 
+@pytest.mark.parametrize("S,H,Hk,D", [(5200, 4, 4, 128), (700, 2, 2, 128), (900, 8, 2, 64), (300, 4, 1, 128)])
+def test_bwd_of_blocks_that_kept_nothing(ssa, S, H, Hk, D):
+    """Zero gradients, every time, beside blocks with one tile: such a CTA is
+    done before its own first loads have arrived."""
+    q, k, v, dout, cu = make([S], H, Hk, D, seed=32)
+    out, lse = ssa.fwd_lse(q, k, v, cu, S)
+    bm = bitmap_for(ssa, [S], H)
+    for _ in range(30):
+        grads = [torch.full_like(t, 7.0) for t in (q, k, v)]
+        ssa.bwd(dout, q, k, v, out, lse, cu, S, decision_bitmap=bm, dq=grads[0], dk=grads[1], dv=grads[2])
+        assert not any(g.any() for g in grads)
+    bm[:, 1, 0] = ~2  # query block 1 keeps tile 1
+    for _ in range(30):
+        dq, dk, dv = ssa.bwd(dout, q, k, v, out, lse, cu, S, decision_bitmap=bm)
+        for g in (dq, dk, dv):
+            assert not g[:128].any() and not g[256:].any() and g[128:256].any()
+    ssa.check_device()
+
+
 def test_bwd_against_differences(ssa):
     """Directional differences of sum(dout * out) in 64 bits at the bf16 inputs."""
     lens, H, Hk, D = [70, 140], 2, 1, 64

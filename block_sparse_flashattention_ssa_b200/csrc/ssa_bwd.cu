@@ -13,7 +13,7 @@
 // core takes Q, K and dO in; sums, statistics and D stay in fp32. Because
 // sum_j dS_rj is nearly zero, what the keys have in common cancels in dQ, but
 // not in its rounding errors: the q role sums up what the rounding of a row's
-// dS added and takes that times the mean key of its own block out again.
+// dS added and takes that times a mean of its own block's keys out again.
 //
 // A first kernel forms D and -L log2 e per row, padded to whole query blocks
 // (rows past a sequence end get -inf, so their probabilities vanish). The
@@ -361,8 +361,8 @@ __device__ __forceinline__ void key_mean(const Params& p, const Unit& u, int hea
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
       const float2 f = unpack_bf16x2(w[c]);
-      sum[i * 8 + 2 * c] = isfinite(f.x) ? f.x : 0.f;
-      sum[i * 8 + 2 * c + 1] = isfinite(f.y) ? f.y : 0.f;
+      sum[i * 8 + 2 * c] = isfinite(f.x) ? f.x * (1.f / 32.f) : 0.f;
+      sum[i * 8 + 2 * c + 1] = isfinite(f.y) ? f.y * (1.f / 32.f) : 0.f;
     }
   }
   // Each step adds lanes o apart and leaves each of them half of the columns,
@@ -385,7 +385,7 @@ __device__ __forceinline__ void key_mean(const Params& p, const Unit& u, int hea
       sum[0] += __shfl_xor_sync(kFull, sum[0], o);
     }
   }
-  mean[warp * kCols + column] = sum[0] * (1.f / 32.f);  // lanes with the same column hold the same sum
+  mean[warp * kCols + column] = sum[0];  // lanes with the same column hold the same sum
 }
 
 // All threads of the cluster; orders shared-memory accesses before it against

@@ -186,6 +186,16 @@ def test_bwd_of_blocks_that_kept_nothing(ssa, S, H, Hk, D):
     ssa.check_device()
 
 
+def test_bwd_of_nothing_beside_the_largest_keys(ssa):
+    q, k, v, dout, cu = make([256], 2, 2, 128, seed=33)
+    k.fill_(torch.finfo(torch.bfloat16).max)
+    q.zero_()  # scores of zero, and sums of keys that would overflow
+    out, lse = ssa.fwd_lse(q, k, v, cu, 256)
+    bm = bitmap_for(ssa, [256], 2)
+    for g in ssa.bwd(dout, q, k, v, out, lse, cu, 256, decision_bitmap=bm):
+        assert not g.any()
+
+
 def test_bwd_against_differences(ssa):
     """Directional differences of sum(dout * out) in 64 bits at the bf16 inputs."""
     lens, H, Hk, D = [70, 140], 2, 1, 64

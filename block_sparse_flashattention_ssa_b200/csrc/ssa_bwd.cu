@@ -53,10 +53,10 @@
 //            the last tile's has been read.
 //
 // Bound by the board's power in long runs (75,600 tokens of 5 heads of 128, dense:
-// 42.9 ms at 1.6 GHz, 853 TFLOP/s of the five products, 1194 of the seven formed
-// here; 8192 x 24 x 128 2.28 ms before the clock drops, 2.62 ms after), by the
+// 43.7 ms at 1.6 GHz, 836 TFLOP/s of the five products, 1171 of the seven formed
+// here; 8192 x 24 x 128 2.25 ms before the clock drops, 2.59 ms after), by the
 // element-wise warps at D = 64 (8192 x 24: 1.85 ms), by the length of the walks
-// and the launches in small batches (1024 x 2 x 64: 15 us).
+// and the launches in small batches (1024 x 2 x 64: 13 us).
 //
 // Every wait is bounded in time; one that runs out records SSA_ERR_TIMEOUT in
 // the status word, the other roles leave at their next wait, in-flight loads

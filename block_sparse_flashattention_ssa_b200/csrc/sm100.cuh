@@ -264,13 +264,6 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
   return r;
 }
 
-// acc += the two bf16 values of `w`, in fp32 (the mixed-precision add of sm_100).
-__device__ __forceinline__ void add_bf16x2(float2& acc, uint32_t w) {
-  asm("{\n .reg .b16 lo, hi;\n mov.b32 {lo, hi}, %2;\n add.rn.f32.bf16 %0, lo, %0;\n add.rn.f32.bf16 %1, hi, %1;\n}"
-      : "+f"(acc.x), "+f"(acc.y)
-      : "r"(w));
-}
-
 __device__ __forceinline__ float2 unpack_bf16x2(uint32_t w) {
   return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
 }

@@ -9,11 +9,16 @@
 //   dQ_r  = c sum_j dS_rj k_j,  dK_j = c sum_r dS_rj q_r
 // The forward's decisions are constants: no gradient flows through them.
 //
-// P and dS are rounded to bf16 for their products, the precision the tensor
-// core takes Q, K and dO in; sums, statistics and D stay in fp32. Because
+// P and dS are rounded to bf16 for the products of dV and dK, the precision the
+// tensor core takes Q, K and dO in; sums, statistics and D stay in fp32. Because
 // sum_j dS_rj is nearly zero, what the keys have in common cancels in dQ, but
-// not in its rounding errors: the q role sums up what the rounding of a row's
-// dS added and takes that times a mean of its own block's keys out again.
+// not in the rounding errors of a row's dS: rounded once, they put dQ off by
+// 0.0026 to 0.0039 of its norm in 64-bit comparisons, against 0.0017 that
+// rounding the result costs. The q role therefore takes dS in two bf16 parts,
+// dS = hi + lo with lo the rounding error of hi, and two products: dQ is off by
+// no more than 0.0017. Each part of dS_rj meets key j alone, so a key without
+// probability leaves no trace (times, rounded once / in two parts: 8192 x 24 x
+// 128 2.49 / 2.73 ms, D = 64 1.74 / 1.90 ms).
 //
 // A first kernel forms D and -L log2 e per row, padded to whole query blocks
 // (rows past a sequence end get -inf, so their probabilities vanish). The
@@ -29,9 +34,9 @@
 // Both roles are one pipeline with the operands exchanged ("fixed" tiles A, B
 // loaded once; "ring" tiles A, B streamed): S = fixA ringA^T, dP = fixB
 // ringB^T, accA += dS ringA, and in the kv role accB += P ringB. S and dP are
-// formed twice (7 products instead of 5), and in exchange every output row has
-// one owner: no atomics, no fp32 dQ in memory, and results that do not depend
-// on the order in which CTAs run.
+// formed twice and dQ's product has two parts (8 products instead of 5); in
+// exchange every output row has one owner: no atomics, no fp32 dQ in memory,
+// and results that do not depend on the order in which CTAs run.
 //
 // Warp 0: TMA producer; warps 1-3: one tcgen05 issuing thread each, for S, for
 // dP and for the accumulating products; warps 4-11: element-wise work, 64
@@ -48,15 +53,16 @@
 //            products that read them are complete: the regions change places
 //            with every tile.
 //   q role, and kv role with D = 64 (accB [320,384)): S in X and Z [384,512) by
-//            turns, dP in Y; dS (and P) replace S. S of a tile is formed as
-//            soon as P and dS of the tile before last are used, dP as soon as
-//            the last tile's has been read.
+//            turns, dP in Y; P and dS, or in the q role dS's two parts, replace
+//            S in the same places. S of a tile is formed as soon as those of
+//            the tile before last are used, dP as soon as the last tile's has
+//            been read.
 //
 // Bound by the board's power in long runs (75,600 tokens of 5 heads of 128, dense:
-// 43.7 ms at 1.6 GHz, 836 TFLOP/s of the five products, 1171 of the seven formed
-// here; 8192 x 24 x 128 2.25 ms before the clock drops, 2.59 ms after), by the
-// element-wise warps at D = 64 (8192 x 24: 1.85 ms), by the length of the walks
-// and the launches in small batches (1024 x 2 x 64: 13 us).
+// 47.3 ms, 774 TFLOP/s of the five products, 1238 of the eight formed here; 8192
+// x 24 x 128 2.73 ms), by the element-wise warps at D = 64 (8192 x 24: 1.90 ms),
+// by the length of the walks and the launches in small batches (1024 x 2 x 64:
+// 13 us).
 //
 // Every wait is bounded in time; one that runs out records SSA_ERR_TIMEOUT in
 // the status word, the other roles leave at their next wait, in-flight loads
@@ -99,7 +105,7 @@ struct Params {
   const int32_t* cu_seqlens;
   const uint32_t* bitmap;  // forward's skip decisions, or NULL: every tile is kept
   __nv_bfloat16 *dq, *dk, *dv;
-  const __nv_bfloat16 *out, *dout, *k, *v;
+  const __nv_bfloat16 *out, *dout, *v;
   const float* lse;
   float* rows;  // [num_heads][units][2][128]: -L log2 e, then -D, per query block
   int* status;
@@ -120,7 +126,8 @@ struct Ctl {
   uint64_t a_full[kAStages], a_empty[kAStages];
   uint64_t b_full[kBStages], b_empty[kBStages];  // b_empty: q role (kv role: a_empty says it)
   // MMA results ready: S of even and odd tiles, dP; element-wise warps: dP in
-  // registers; P (kv role) and dS of even and odd tiles stored. Two barriers
+  // registers; P (kv role) or dS's upper part (q role), and dS or its lower part,
+  // of even and odd tiles stored. Two barriers
   // where the side that completes them may be a tile ahead of the side that
   // looks (the S issuer of the element-wise warps with three score regions,
   // these of the accumulating issuer): a single one would have gone round.
@@ -344,50 +351,6 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
       : "memory");
 }
 
-// Mean key of this block: of 32 of its rows, evenly spread (enough to hold what
-// the keys have in common), finite values only (the dQ of a row that saw others
-// is not finite anyway). Eight warps take D / 8 columns each; one row per lane.
-template <int D>
-__device__ __forceinline__ void key_mean(const Params& p, const Unit& u, int head, int warp, int lane, float* mean) {
-  constexpr int kCols = D / 8;
-  const int rows = min(kT, u.S - u.block * kT);
-  const int64_t token = u.start + u.block * kT + ((lane * rows) >> 5);
-  const uint4* k = reinterpret_cast<const uint4*>(p.k + (token * p.num_kv_heads + head) * D + warp * kCols);
-  float sum[kCols];
-#pragma unroll
-  for (int i = 0; i < kCols / 8; ++i) {
-    const uint4 v = k[i];
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      const float2 f = unpack_bf16x2(w[c]);
-      sum[i * 8 + 2 * c] = isfinite(f.x) ? f.x * (1.f / 32.f) : 0.f;
-      sum[i * 8 + 2 * c + 1] = isfinite(f.y) ? f.y * (1.f / 32.f) : 0.f;
-    }
-  }
-  // Each step adds lanes o apart and leaves each of them half of the columns,
-  // until one is left; then the lanes that share it add up.
-  int column = 0;
-#pragma unroll
-  for (int step = 0; step < 5; ++step) {
-    const int o = 16 >> step, n = kCols >> (step + 1);  // constants, unrolled
-    const bool upper = (lane & o) != 0;
-    if (n > 0) {
-#pragma unroll
-      for (int i = 0; i < kCols / 2; ++i) {
-        if (i < n) {
-          const float send = upper ? sum[i] : sum[n + i], keep = upper ? sum[n + i] : sum[i];
-          sum[i] = keep + __shfl_xor_sync(kFull, send, o);
-        }
-      }
-      column += upper ? n : 0;
-    } else {
-      sum[0] += __shfl_xor_sync(kFull, sum[0], o);
-    }
-  }
-  mean[warp * kCols + column] = sum[0];  // lanes with the same column hold the same sum
-}
-
 // All threads of the cluster; orders shared-memory accesses before it against
 // those after it. (Every path to it is bounded in time.)
 __device__ __forceinline__ void cluster_sync() {
@@ -434,9 +397,9 @@ __device__ __forceinline__ void run_role(const CUtensorMap* tmFixA, const CUtens
   auto ds_full = [&](int j) { return smem_u32(&ctl.ds_full[j & 1]); };  // phase j >> 1
   const uint32_t fix_full = smem_u32(&ctl.fix_full), acc_full = smem_u32(&ctl.acc_full);
   // Tile j's ring A stage is free, which also says that the products that read
-  // its P and dS, and (kv role) its ring B stage and row values, are complete.
+  // its P and dS (or dS's parts), and (kv role) its ring B stage and row values, are complete.
   auto acc_done = [&](int j) { return smem_u32(&ctl.a_empty[j % kAStages]); };  // phase j / kAStages
-  // The region of S of tile j, then of its dS and (kv role) P; and that of dP.
+  // The region of S of tile j, then of its P and dS or of dS's parts; and that of dP.
   auto col_s = [&](int j) { return j & 1 ? (kThree ? kColZ : kColY) : kColX; };
   auto col_dp = [&](int j) { return kThree || !(j & 1) ? kColY : kColX; };
 
@@ -589,16 +552,14 @@ __device__ __forceinline__ void run_role(const CUtensorMap* tmFixA, const CUtens
           if (Q) tc_commit(b_empty(j % kBStages));
         }
       } else {  // kAccWarp
-        // q role: dQ += dS(j) K_j. kv role: dV += P(j)^T dO_j, dK += dS(j)^T Q_j.
+        // q role: dQ += hi(j) K_j, dQ += lo(j) K_j. kv role: dV += P(j)^T dO_j, dK += dS(j)^T Q_j.
         for (int j = 0; ok && has(j); ++j) {
-          if (!Q) {
-            if (!(ok = wait(p_full(j), (j >> 1) & 1))) break;
-            tc_fence_after();
-            accumulate(kColAccB, col_s(j), ring_b(j), j > 0);
-          }
+          if (!(ok = wait(p_full(j), (j >> 1) & 1))) break;
+          tc_fence_after();
+          accumulate(Q ? kColAccA : kColAccB, col_s(j), Q ? ring_a(j) : ring_b(j), j > 0);
           if (!(ok = wait(ds_full(j), (j >> 1) & 1))) break;
           tc_fence_after();
-          accumulate(kColAccA, col_s(j) + (Q ? 0 : 32), ring_a(j), j > 0);
+          accumulate(kColAccA, col_s(j) + 32, ring_a(j), Q || j > 0);
           tc_commit(acc_done(j));
         }
         if (ok) tc_commit(acc_full);
@@ -615,18 +576,13 @@ __device__ __forceinline__ void run_role(const CUtensorMap* tmFixA, const CUtens
     const int row = (warp & 3) * 32 + lane;
     const uint32_t lanes = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
     float row_bias = 0.f, row_ndelta = 0.f;  // q role: this thread's row
-    const float2 zero = make_float2(0.f, 0.f);
-    float2 exact[2] = {zero, zero}, rounded[2] = {zero, zero};  // q role: sums of its dS before and after rounding
-    float* mean_key = reinterpret_cast<float*>(smem + L::kRows);       // q role: [D], then the rows' sums [2][128]
     if (Q) {
-      key_mean<D>(p, u, head / group, warp - kEwWarp, lane, mean_key);
-      named_barrier_sync(1, kEwThreads);
       wait_for_rows();
       const float* r = p.rows + (static_cast<int64_t>(head) * p.units + u.gqb0 + u.block) * (2 * kT);
       row_bias = r[row];
       row_ndelta = r[kT + row];
     }
-    const float2 c2 = make_float2(p.c2, p.c2);
+    const float2 c2 = make_float2(p.c2, p.c2), minus_one = make_float2(-1.f, -1.f);
     // Waits are looked at ahead of their time, over work that does not need
     // them. The check right behind the arrival on dp_done also keeps the
     // compiler from moving that arrival behind the arithmetic that follows it.
@@ -717,13 +673,23 @@ __device__ __forceinline__ void run_role(const CUtensorMap* tmFixA, const CUtens
         pk[2 * i] = pack_bf16x2(x.x, x.y);
         pk[2 * i + 1] = pack_bf16x2(y.x, y.y);
         if (Q) {
-          exact[0] = fadd2(exact[0], x);
-          exact[1] = fadd2(exact[1], y);
-          add_bf16x2(rounded[0], pk[2 * i]);
-          add_bf16x2(rounded[1], pk[2 * i + 1]);
+          s[4 * i] = __float_as_uint(x.x);
+          s[4 * i + 1] = __float_as_uint(x.y);
+          s[4 * i + 2] = __float_as_uint(y.x);
+          s[4 * i + 3] = __float_as_uint(y.y);
         }
       }
-      tmem_st_x32(lanes + col_s(j) + half * 64 + (Q ? 0 : 32), pk);
+      if (Q) {
+        tmem_st_x32(lanes + col_s(j) + half * 64, pk);
+        warp_arrive(p_full(j), lane);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {  // what rounding left of dS, exact in fp32
+          const float2 l = ffma2(unpack_bf16x2(pk[i]), minus_one,
+                                 make_float2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])));
+          pk[i] = pack_bf16x2(l.x, l.y);
+        }
+      }
+      tmem_st_x32(lanes + col_s(j) + half * 64 + 32, pk);
       warp_arrive(ds_full(j), lane);
       valid = valid_next;
       sa = sa_next;
@@ -732,14 +698,6 @@ __device__ __forceinline__ void run_role(const CUtensorMap* tmFixA, const CUtens
 
     // Epilogue: this thread's row and half of the D columns of each accumulator.
     const bool any = j > 0;  // no tile was kept: the gradients are zero
-    float excess = 0.f;      // q role: of the row, over both halves of its columns
-    if (Q) {                 // every element-wise warp comes here, with or without an error
-      float* sums = mean_key + D;
-      sums[half * kT + row] = ((rounded[0].x - exact[0].x) + (rounded[0].y - exact[0].y)) +
-                               ((rounded[1].x - exact[1].x) + (rounded[1].y - exact[1].y));
-      named_barrier_sync(1, kEwThreads);
-      excess = sums[row] + sums[kT + row];
-    }
     if (ok) ok = warp_wait(acc_full, 0, abort_flag, p.status);
     // Results are staged over the tiles: all loads must have landed. Where tiles
     // were walked the accumulators say so; where none was, the fixed tiles may
@@ -755,11 +713,7 @@ __device__ __forceinline__ void run_role(const CUtensorMap* tmFixA, const CUtens
           uint32_t o[32];
           tmem_ld_x32(lanes + (a ? kColAccB : kColAccA) + half * (D / 2) + ch * 32, o);
 #pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            float x = any ? __uint_as_float(o[i]) : 0.f;
-            if (Q) x = fmaf(-excess, mean_key[half * (D / 2) + ch * 32 + i], x);
-            o[i] = __float_as_uint(x);
-          }
+          for (int i = 0; i < 32; ++i) o[i] = any ? o[i] : 0u;
           if (split > 1) {
             uint4* part = reinterpret_cast<uint4*>(smem + ((a * kT + row) * kPartRow + half * (D / 2) + ch * 32) * 4);
 #pragma unroll
@@ -1017,7 +971,6 @@ int internal::launch_backward(const Backward& a, cudaStream_t stream) {
   p.dv = static_cast<__nv_bfloat16*>(a.dv);
   p.out = static_cast<const __nv_bfloat16*>(a.out);
   p.dout = static_cast<const __nv_bfloat16*>(a.dout);
-  p.k = static_cast<const __nv_bfloat16*>(a.k);
   p.v = static_cast<const __nv_bfloat16*>(a.v);
   p.lse = a.lse;
   p.rows = static_cast<float*>(a.workspace);

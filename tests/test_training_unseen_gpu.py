@@ -1,0 +1,87 @@
+"""Gradients depend on what a row sees and on nothing else: keys without
+probability, tiles that were skipped, rows that take no part and memory past a
+sequence leave no trace, whatever stands there."""
+import math
+
+import pytest
+
+from tests import training_ref as ref
+from tests.test_training_gpu import bitmap_for, make, same, ssa  # noqa: F401  (ssa: the fixture)
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+
+# Batches whose blocks are walked by one CTA each (many heads) and by clusters.
+SHAPES = [([300], 2, 2, 128), ([300], 4, 2, 64), ([700, 200], 16, 16, 128), ([700, 200], 24, 12, 64)]
+
+
+def formula(ssa, dout, q, k, v, out, lse, cu, lens, bitmap=None):  # noqa: F811
+    grads = ssa.bwd(dout, q, k, v, out, lse, cu, max(lens), decision_bitmap=bitmap)
+    ssa.check_device()
+    want, bound = ref.backward(dout, q, k, v, out, lse, lens, bitmap)
+    seen = ref.bound_dq(dout, q, k, v, out, lse, lens, bitmap)
+    for g, w, b, name in zip(grads, want, (seen, *bound[1:]), ("dq", "dk", "dv")):
+        ref.check(g, w, b, name)
+    return grads
+
+
+@pytest.mark.parametrize("lens,H,Hk,D", SHAPES, ids=str)
+def test_keys_without_probability(ssa, lens, H, Hk, D):  # noqa: F811
+    """Every block's first key, and a whole block of keys, at scores at which
+    fp32 and fp64 exponentials are zero: their size does not matter by a bit."""
+    q, k, v, dout, cu = make(lens, H, Hk, D, seed=40)
+    q[..., 0] = 128.0  # scores along the first dimension: c * 128 * k[0]
+    first = [t for lo, hi in zip(cu.tolist(), cu.tolist()[1:]) for t in range(lo, hi, 128)]
+    for unseen in (first, list(range(128, 256))):
+        seen = torch.ones(k.shape[0], dtype=torch.bool)
+        seen[unseen] = False
+        before = None
+        for size in (1e3, 1e5, 1e30):
+            kk = k.clone()
+            kk[..., 0] = kk[..., 0] / 128  # the others' scores stay in an ordinary range
+            kk[unseen, :, 0] = -size
+            vv = v.clone()
+            vv[unseen] = vv[unseen] * size ** 0.5
+            out, lse = ssa.fwd_lse(q, kk, vv, cu, max(lens))
+            grads = formula(ssa, dout, q, kk, vv, out, lse, cu, lens)
+            assert not grads[1][unseen].any() and not grads[2][unseen].any()
+            if before is not None:
+                assert same(out, before[0])
+                assert all(torch.equal(a, b) for a, b in zip(grads, before[1:]))
+            before = (out, *grads)
+
+
+@pytest.mark.parametrize("lens,H,Hk,D", SHAPES, ids=str)
+def test_keys_of_skipped_tiles(ssa, lens, H, Hk, D):  # noqa: F811
+    """Query block b skips tile b (its own rows), and every block of a sequence
+    of three tiles or more skips tile 1: the keys there may have any size."""
+    q, k, v, dout, cu = make(lens, H, Hk, D, seed=41)
+    bm = bitmap_for(ssa, lens, H)
+    bm.zero_()
+    unit = 0
+    for n in lens:
+        for b in range((n + 127) // 128):
+            bm[:, unit, 0] = (1 << b) | (2 if n > 256 else 0)
+            unit += 1
+    # out and lse of the kept tiles, by the formula
+    o, L, _, _ = ref.forward(q, k, v, lens, bm)
+    out, lse = o.bfloat16().cuda(), L.float().cuda()
+    rows = slice(128, 256)  # tile 1 of the first sequence: skipped by every block
+    before = None
+    for offset in (0.0, 30.0, 1e4, 1e30):
+        kk, vv = k.clone(), v.clone()
+        kk[rows] += offset
+        vv[rows] += offset
+        grads = formula(ssa, dout, q, kk, vv, out, lse, cu, lens, bm)
+        assert not grads[1][rows].any() and not grads[2][rows].any()
+        if before is not None:
+            assert all(torch.equal(a, b) for a, b in zip(grads, before))
+        before = grads
+    # each block's own keys, which other blocks see: its own dQ does not change
+    kk, vv = k.clone(), v.clone()
+    kk[:128] += 1e4
+    vv[:128] += 1e4
+    dq = ssa.bwd(dout, q, kk, vv, out, lse, cu, max(lens), decision_bitmap=bm)[0]
+    ssa.check_device()
+    assert torch.equal(dq[:128], before[0][:128])

@@ -178,3 +178,31 @@ def rotate(x, positions, inv_freq, sections, interleaved, scale, transpose):
     e = 2 * math.pi * 2.0 ** -24 + 6 * E + angle.abs()[:, None] * 2.0 ** -50
     b[..., left] = b[..., right] = (a0.abs() + b0.abs()) * abs(scale) * e
     return y, b + U * (y.abs() + b) * (1 if n else 0) + 1e-37
+
+
+def bound_dq(dout, q, k, v, out, lse, lens, bitmap=None, scale=0.0):
+    """dQ's bound of backward() over the keys a row sees alone: no term for any
+    other key."""
+    dout, q, k, v, out, lse = (t.double().cpu() for t in (dout, q, k, v, out, lse))
+    total, H, D = q.shape
+    G = H // k.shape[1]
+    c = scale if scale > 0 else D ** -0.5
+    dq, bq = torch.zeros(total, H, D, dtype=torch.float64), torch.zeros(total, H, D, dtype=torch.float64)
+    for h, lo, hi, gqb in heads(lens, H=H):
+        n = hi - lo
+        keep = None if bitmap is None else keep_of(bitmap, h, gqb, n)
+        s, err = _scores(q, k, lo, hi, h, h // G, c, keep)
+        L = lse[h, lo:hi]
+        P = torch.where(torch.isinf(L)[:, None], torch.zeros_like(s), torch.exp(s - L[:, None]))
+        seen = P > 0
+        zero = torch.zeros_like(s)
+        K, V, dO, O = k[lo:hi, h // G], v[lo:hi, h // G], dout[lo:hi, h], out[lo:hi, h]
+        dev = (dO @ V.T - (dO * O).sum(1, keepdim=True)).where(seen, zero)
+        dS = P * dev
+        rho = (err + 8 * E * (s.abs() + L.abs()[:, None] + 1)).where(seen, zero)
+        mag = (dO.abs() @ V.abs().T + (dO.abs() * O.abs()).sum(1, keepdim=True)).where(seen, zero)
+        eS = P * rho * dev.abs() + P * (1 + rho) * (D + 2) * E * mag
+        rS = eS + U * (dS.abs() + eS)  # after rounding to bf16
+        dq[lo:hi, h] = c * (dS @ K)
+        bq[lo:hi, h] = c * (rS @ K.abs() + n * E * ((dS.abs() + rS) @ K.abs()))
+    return bq + (U + 4 * E) * (dq.abs() + bq) + 1e-37

@@ -21,7 +21,7 @@
 // 128 2.49 / 2.73 ms, D = 64 1.74 / 1.90 ms).
 //
 // A first kernel forms D and -L log2 e per row, padded to whole query blocks
-// (rows past a sequence end get -inf, so their probabilities vanish). The
+// (rows past a sequence end get -inf, as rows whose L is -inf do). The
 // main kernel's CTAs each own 128 output rows and walk the other side's tiles:
 //   kv role: 128 rows of K, V of one K/V head against every query block of the
 //            sequence and every query head of its group that kept the tile;
@@ -284,6 +284,17 @@ __device__ __forceinline__ void wait_for_rows() {
   asm volatile("griddepcontrol.wait;\n fence.proxy.async.global;" ::: "memory");
 }
 
+// A row whose bias -L log2 e is -inf takes no part: one that saw nothing, or one
+// past the sequence end. What its q, dO and O hold may be anything, so the main
+// kernel's kv role sets its elements aside (a zero probability times NaN is NaN).
+// To look for such rows only where there are some inside the sequence, the lowest
+// bit of the bias of a block's first row says so (and costs that row at most
+// 2^-23 of its bias, like a rounding).
+__device__ __forceinline__ bool takes_no_part(float bias) { return bias == -INFINITY; }
+__device__ __forceinline__ bool some_take_no_part(float first_bias) {
+  return takes_no_part(first_bias) || (__float_as_uint(first_bias) & 1u);
+}
+
 // -D_r = -dO_r.O_r and -L_r log2 e of one query block and head; D / 8 lanes per
 // row, 16 bytes of dO and O each. Bound by the read of dO and O. The one row of
 // a sequence of length one gets dP - D = dO.(v - O) in place of -D: the forward
@@ -303,16 +314,27 @@ __global__ void __launch_bounds__(256) rows_kernel(const __grid_constant__ Param
   float* dst = p.rows + (static_cast<int64_t>(head) * p.units + u.gqb0 + u.block) * (2 * kT);
   const int64_t base = (static_cast<int64_t>(u.start + u.block * kT) * p.num_heads + head) * D + part * 8;
   uint4 a[kSteps], b[kSteps];
+  float bias[kSteps];
+  bool none = false;
 #pragma unroll
   for (int i = 0; i < kSteps; ++i) {
     const int r = r0 + i * kRowsAtOnce;
     a[i] = b[i] = make_uint4(0, 0, 0, 0);
+    bias[i] = -INFINITY;
     if (r < rows) {
       const int64_t at = base + static_cast<int64_t>(r) * p.num_heads * D;
       a[i] = *reinterpret_cast<const uint4*>(p.dout + at);
       b[i] = *reinterpret_cast<const uint4*>(p.out + at);
+      bias[i] = -p.lse[static_cast<int64_t>(head) * p.total_tokens + u.start + u.block * kT + r] * kLog2e;
     }
   }
+#pragma unroll
+  for (int i = 0; i < kSteps; ++i) {  // an lse of -inf has no reciprocal sum; one of +inf no probability
+    if (isinf(bias[i])) bias[i] = -INFINITY;
+    none = none || (r0 + i * kRowsAtOnce < rows && takes_no_part(bias[i]));
+  }
+  const uint32_t some = __syncthreads_or(none) ? 1u : 0u;
+  if (r0 == 0 && !takes_no_part(bias[0])) bias[0] = __uint_as_float((__float_as_uint(bias[0]) & ~1u) | some);
 #pragma unroll
   for (int i = 0; i < kSteps; ++i) {
     const int r = r0 + i * kRowsAtOnce;
@@ -332,13 +354,8 @@ __global__ void __launch_bounds__(256) rows_kernel(const __grid_constant__ Param
 #pragma unroll
     for (int o = kLanes / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
     if (part == 0) {
-      float bias = -INFINITY;  // past the sequence, or a row that saw nothing: no probability
-      if (r < rows) {
-        const float L = p.lse[static_cast<int64_t>(head) * p.total_tokens + u.start + u.block * kT + r];
-        if (L != -INFINITY) bias = -L * kLog2e;
-      }
-      dst[r] = bias;
-      dst[kT + r] = -sum;
+      dst[r] = bias[i];
+      dst[kT + r] = takes_no_part(bias[i]) ? 0.f : -sum;
     }
   }
 }
@@ -592,20 +609,25 @@ __device__ __forceinline__ void run_role(const CUtensorMap* tmFixA, const CUtens
     int sa = 0, a_phase = 0;  // j % kAStages, (j / kAStages) & 1
     for (; ok && valid >= 0; ++j) {
       const int sa_next = sa + 1 == kAStages ? 0 : sa + 1, a_phase_next = a_phase ^ (sa_next == 0 ? 1 : 0);
-      const float* rows = reinterpret_cast<const float*>(smem + L::kRows + (j % kBStages) * L::kRowBytes) + half * 64;
+      const float* tile_rows = reinterpret_cast<const float*>(smem + L::kRows + (j % kBStages) * L::kRowBytes);
+      const float* rows = tile_rows + half * 64;
       if (!Q && !(ok = warp_wait_seen(rows_seen, b_full(j % kBStages), (j / kBStages) & 1, abort_flag, p.status))) break;
+      const float first_bias = Q ? 0.f : tile_rows[0];
       if (!(ok = warp_wait_seen(s_seen, s_full(j), (j >> 1) & 1, abort_flag, p.status))) break;
       tc_fence_after();
       uint32_t s[64];
       tmem_ld_x64_async(lanes + col_s(j) + half * 64, s);
       const bool a_seen = mbar_test_wait(a_full(sa_next), a_phase_next);
-      if (valid < kT) {
-        // The tile ends past the sequence. Its rows out there are summation
-        // rows of the accumulating products: they must be zeros, not whatever
-        // memory holds (NaN times a zero probability is NaN).
-        const int words = (kT - valid) * 8;  // 16-byte words of a chunk's rows past the end
+      const bool gaps = !Q && some_take_no_part(first_bias), masked = gaps || valid < kT;
+      if (masked) {
+        // The tile ends past the sequence, or (kv role) rows of it take no part.
+        // Those are summation rows of the accumulating products: they must be
+        // zeros, not whatever memory holds (NaN times a zero probability is NaN).
+        const int first = gaps ? 0 : valid;
+        const int words = (kT - first) * 8;  // 16-byte words of a chunk's rows from there on
         for (int i = threadIdx.x - 32 * kEwWarp; i < L::kChunks * words; i += kEwThreads) {
-          const int at = (i / words) * L::kChunkBytes + valid * 128 + (i % words) * 16;
+          const int at = (i / words) * L::kChunkBytes + first * 128 + (i % words) * 16;
+          if (!Q && !takes_no_part(tile_rows[first + i % words / 8])) continue;
           *reinterpret_cast<uint4*>(smem + L::kRingA + sa * L::kTileBytes + at) = make_uint4(0, 0, 0, 0);
           if (!Q)
             *reinterpret_cast<uint4*>(smem + L::kRingB + (j % kBStages) * L::kTileBytes + at) = make_uint4(0, 0, 0, 0);
@@ -613,10 +635,10 @@ __device__ __forceinline__ void run_role(const CUtensorMap* tmFixA, const CUtens
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       }
       tmem_wait_ld_tied(s);
-      if (valid < kT) {  // no probability past the end, whatever stands there
+      if (masked) {  // no probability there, whatever stands there
 #pragma unroll
         for (int i = 0; i < 64; ++i)
-          if (half * 64 + i >= valid) s[i] = __float_as_uint(-INFINITY);
+          if (Q ? half * 64 + i >= valid : takes_no_part(rows[i])) s[i] = __float_as_uint(-INFINITY);
       }
       const bool dp_seen = mbar_test_wait(dp_full, j & 1);
       // P = 2^(c2 S - L log2 e)
@@ -654,10 +676,10 @@ __device__ __forceinline__ void run_role(const CUtensorMap* tmFixA, const CUtens
       if (kThree) s_seen = mbar_test_wait(s_full(j + 1), ((j + 1) >> 1) & 1);
       if (!Q)
         rows_seen = mbar_test_wait(b_full((j + 1) % kBStages), ((j + 1) / kBStages) & 1);
-      if (valid < kT) {
+      if (masked) {
 #pragma unroll
         for (int i = 0; i < 64; ++i)
-          if (half * 64 + i >= valid) d[i] = 0u;
+          if (Q ? half * 64 + i >= valid : takes_no_part(rows[i])) d[i] = 0u;
         if (u.S == 1) d[0] = half == 0 ? 0u : d[0];  // -D holds dP - D (see rows_kernel)
       }
 #pragma unroll
@@ -698,6 +720,7 @@ __device__ __forceinline__ void run_role(const CUtensorMap* tmFixA, const CUtens
 
     // Epilogue: this thread's row and half of the D columns of each accumulator.
     const bool any = j > 0;  // no tile was kept: the gradients are zero
+    const bool part = any && !(Q && takes_no_part(row_bias));  // nor has a row that takes no part one
     if (ok) ok = warp_wait(acc_full, 0, abort_flag, p.status);
     // Results are staged over the tiles: all loads must have landed. Where tiles
     // were walked the accumulators say so; where none was, the fixed tiles may
@@ -713,7 +736,7 @@ __device__ __forceinline__ void run_role(const CUtensorMap* tmFixA, const CUtens
           uint32_t o[32];
           tmem_ld_x32(lanes + (a ? kColAccB : kColAccA) + half * (D / 2) + ch * 32, o);
 #pragma unroll
-          for (int i = 0; i < 32; ++i) o[i] = any ? o[i] : 0u;
+          for (int i = 0; i < 32; ++i) o[i] = part ? o[i] : 0u;
           if (split > 1) {
             uint4* part = reinterpret_cast<uint4*>(smem + ((a * kT + row) * kPartRow + half * (D / 2) + ch * 32) * 4);
 #pragma unroll

@@ -260,7 +260,9 @@ int ssa_fwd_lse(const void* q, const void* k, const void* v, const int32_t* cu_s
  * dQ, whatever finite values the key and its v hold.
  * Results do not depend on the order of execution.
  *   dout, out         device bf16 [total_tokens, num_heads, head_dim]
- *   lse               as ssa_fwd_lse wrote it (a row with -inf takes no part)
+ *   lse               as ssa_fwd_lse wrote it; a row with an infinity takes no
+ *                     part: its dq is zero, and its q, out and dout, whatever
+ *                     they hold, have no effect
  *   decision_bitmap   as ssa_fwd_lse wrote it for the same max_seqlen, or NULL
  *                     when every tile was kept; num_qblocks is its Q
  *   dq                device bf16 [total_tokens, num_heads, head_dim]

@@ -85,3 +85,33 @@ def test_keys_of_skipped_tiles(ssa, lens, H, Hk, D):  # noqa: F811
     dq = ssa.bwd(dout, q, kk, vv, out, lse, cu, max(lens), decision_bitmap=bm)[0]
     ssa.check_device()
     assert torch.equal(dq[:128], before[0][:128])
+
+
+@pytest.mark.parametrize("lens,H,Hk,D", SHAPES + [([1, 128, 5], 2, 1, 64)], ids=str)
+@pytest.mark.parametrize("tsf", [0.0, 200.0])
+def test_rows_that_take_no_part(ssa, lens, H, Hk, D, tsf):  # noqa: F811
+    """A row whose lse is -inf has no gradient and no part in any other,
+    whatever its q, out and dout hold: single rows (a block's first and last
+    among them), a whole block, and one row of one head alone."""
+    q, k, v, dout, cu = make(lens, H, Hk, D, seed=42, amp=3.0)
+    bm = bitmap_for(ssa, lens, H) if tsf else None
+    out, lse = ssa.fwd_lse(q, k, v, cu, max(lens), tsf, decision_bitmap=bm)
+    total = sum(lens)
+    dead = torch.zeros(H, total, dtype=torch.bool, device="cuda")
+    dead[:, [t for t in (0, 5, 127, 130, total - 1) if t < total]] = True
+    dead[:, 128:256] |= total > 256
+    dead[0, total // 2] = True
+    lse = lse.masked_fill(dead, -math.inf)
+    rows = dead.T[..., None]
+    finite = [t.masked_fill(rows, 0.0) for t in (dout, q, out)]
+    want, bound = ref.backward(finite[0], finite[1], k, v, finite[2], lse, lens, bm)
+    plain = ssa.bwd(finite[0], finite[1], k, v, finite[2], lse, cu, max(lens), decision_bitmap=bm)
+    for g, w, b, name in zip(plain, want, bound, ("dq", "dk", "dv")):
+        ref.check(g, w, b, name)
+    for bad in (math.nan, math.inf, torch.finfo(torch.bfloat16).max):
+        for which in ((2,), (0, 2), (0, 1, 2)):
+            args = [t.masked_fill(rows, bad) if i in which else t for i, t in enumerate((dout, q, out))]
+            grads = ssa.bwd(args[0], args[1], k, v, args[2], lse, cu, max(lens), decision_bitmap=bm)
+            ssa.check_device()
+            assert not grads[0].masked_select(rows).any()
+            assert all(torch.equal(a, b) for a, b in zip(grads, plain)), (bad, which)

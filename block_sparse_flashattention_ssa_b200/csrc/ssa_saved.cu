@@ -5,9 +5,10 @@
 // code = E4M3(x / s), nearest even. A power of two costs nothing in relative
 // precision (E4M3 has exponents to spare) and makes both directions exact but
 // for that one rounding: x / s is exact, and s times an E4M3 value (4
-// significant bits) is exact in bf16. A value that is not finite gets the
-// NaN code and does not count towards the scale, so an overflow in the
-// forward still shows in the gradients.
+// significant bits) is exact in bf16. At the largest scale, 2^120, the code
+// stops at 240: the next one, 256, would restore to 2^128, past bf16. A value
+// that is not finite gets the NaN code and does not count towards the scale, so
+// an overflow in the forward still shows in the gradients.
 //
 // Saving is one pass: a CTA holds the 128 x D tile of its head (of two heads
 // with D = 64) in registers between the maximum and the conversion. Bound by
@@ -28,6 +29,10 @@ namespace {
 constexpr int kT = SSA_TILE;
 constexpr int kThreads = 256;
 constexpr int kMinExponent = -100;  // of the scale: its reciprocal and its products stay normal
+constexpr int kMaxExponent = 120;   // of the scale: that of the largest bf16 values
+
+// Finite values only: what is not finite stays so.
+__device__ __forceinline__ float up_to_240(float y) { return fabsf(y) > 240.f && !isinf(y) ? copysignf(240.f, y) : y; }
 
 // blockIdx.x: block of 128 tokens; blockIdx.y: 128 / D heads.
 template <int D>
@@ -106,6 +111,10 @@ __global__ void __launch_bounds__(kThreads) save_kernel(const __nv_bfloat16* __r
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       float lo = __uint_as_float(w[k] << 16) * inv, hi = __uint_as_float(w[k] & 0xFFFF0000u) * inv;
+      if (e == kMaxExponent) {
+        lo = up_to_240(lo);
+        hi = up_to_240(hi);
+      }
       if (infinite) {
         if (isinf(lo)) lo = __int_as_float(0x7FC00000);
         if (isinf(hi)) hi = __int_as_float(0x7FC00000);

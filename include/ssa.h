@@ -284,8 +284,9 @@ int ssa_bwd(const void* dout, const void* q, const void* k, const void* v, const
 /*
  * Activations saved in 8 bits: E4M3 codes and one scale per 128 consecutive
  * tokens and head, the smallest power of two s with max |x| <= 448 s (1 where
- * all are zero, at least 2^-100), code = E4M3(x / s) to nearest even. A value
- * that is not finite gets the NaN code and does not count for the scale.
+ * all are zero, at least 2^-100), code = E4M3(x / s) to nearest even, but at
+ * most 240 at s = 2^120, where 256 s is past bf16. A value that is not finite
+ * gets the NaN code and does not count for the scale.
  * ssa_restore_fp8 returns s * decode(code), exact in bf16.
  *   x       device bf16 [total_tokens, num_heads, head_dim], 16-byte aligned;
  *           head_dim 64 or 128

@@ -214,9 +214,9 @@ __device__ __forceinline__ void warp_arrive(uint32_t bar, int lane) {
 __device__ void locate(const Params& p, int x, int lane, bool report, Unit& u) {
   if (p.batch == 1) {
     if (lane == 0) {
-      const int lo = p.cu_seqlens[0], hi = p.cu_seqlens[1], len = hi - lo;
-      const bool in = lo >= 0 && len >= 0 && hi <= p.total_tokens;
-      const int nq = in ? (len + kT - 1) / kT : 0;
+      const int lo = p.cu_seqlens[0], hi = p.cu_seqlens[1];
+      const bool in = lo >= 0 && hi >= lo && hi <= p.total_tokens;  // before the difference, which may pass 32 bits
+      const int len = in ? hi - lo : 0, nq = (len + kT - 1) / kT;
       const bool bad = !in || (p.bitmap && nq > p.max_tiles) || (p.nq_check >= 0 && nq != p.nq_check);
       if (bad && report) atomicOr(p.status, kStatusDeviceArg);
       u = Unit{!bad && x < nq ? 0 : -1, x, len, lo, 0, nq};
@@ -230,9 +230,10 @@ __device__ void locate(const Params& p, int x, int lane, bool report, Unit& u) {
     if (b < p.batch) {
       lo = p.cu_seqlens[b];
       const int hi = p.cu_seqlens[b + 1];
-      len = hi - lo;
-      if (lo < 0 || len < 0 || hi > p.total_tokens) bad = 1;
-      nq = bad ? 0 : (len + kT - 1) / kT;
+      const bool in = lo >= 0 && hi >= lo && hi <= p.total_tokens;
+      if (!in) bad = 1;
+      len = in ? hi - lo : 0;
+      nq = (len + kT - 1) / kT;
       if (p.bitmap && nq > p.max_tiles) bad = 1;
     }
     int off = nq;  // inclusive prefix sum in sequence order

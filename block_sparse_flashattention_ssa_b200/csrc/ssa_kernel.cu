@@ -252,8 +252,8 @@ __device__ void locate_unit(const Params& p, bool need_max, int lane, Ctl& ctl) 
     if (b < p.batch) {
       lo = p.cu_seqlens[b];
       const int hi = p.cu_seqlens[b + 1];
-      len = hi - lo;
-      if (lo < 0 || len < 0 || hi > p.total_tokens) bad = 1;
+      if (lo < 0 || hi < lo || hi > p.total_tokens) bad = 1;  // before the difference, which may pass 32 bits
+      len = bad ? 0 : hi - lo;
       nq = (len + kBM - 1) / kBM;
       np = (nq + 1) / 2;
       if (need_max && nq > p.max_tiles) bad = 1;
@@ -290,11 +290,11 @@ __device__ void locate_unit(const Params& p, bool need_max, int lane, Ctl& ctl) 
     if (prev < 0) bad = 1;
     for (int b = 0; b < p.batch && !bad; ++b) {
       const int nxt = p.cu_seqlens[b + 1];
-      const int len = nxt - prev;
-      if (len < 0 || nxt > p.total_tokens) {
+      if (nxt < prev || nxt > p.total_tokens) {
         bad = 1;
         break;
       }
+      const int len = nxt - prev;
       const int nq = (len + kBM - 1) / kBM;
       const int np = (nq + 1) / 2;
       if (need_max && nq > p.max_tiles) bad = 1;

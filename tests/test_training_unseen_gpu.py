@@ -115,3 +115,45 @@ def test_rows_that_take_no_part(ssa, lens, H, Hk, D, tsf):  # noqa: F811
             ssa.check_device()
             assert not grads[0].masked_select(rows).any()
             assert all(torch.equal(a, b) for a, b in zip(grads, plain)), (bad, which)
+
+
+@pytest.mark.parametrize("tsf", [0.0, 30.0])
+@pytest.mark.parametrize("H,Hk,D", [(2, 1, 128), (16, 16, 128), (16, 16, 64)])
+def test_memory_past_a_sequence_while_skipping(ssa, tsf, H, Hk, D):  # noqa: F811
+    """NaN and infinities behind the last sequence and in a sequence between two
+    others, with the forward's own decisions: last tiles that end inside and are
+    kept by both, one or none of the forward's two query blocks of a CTA."""
+    lens, extra = [1100, 130, 70, 640, 1], 90
+    q, k, v, dout, cu = make(lens, H, Hk, D, seed=43, extra=extra, amp=3.0)
+    n, lo, hi = sum(lens), 1230, 1300
+    ends = []
+
+    def run(q, k, v, dout):
+        bm = bitmap_for(ssa, lens, H)
+        out, lse = torch.full_like(q, 3.0), torch.full((H, n + extra), 5.0, device="cuda")
+        ssa.fwd_lse(q, k, v, cu, max(lens), tsf, out=out, lse=lse, decision_bitmap=bm)
+        grads = [torch.full_like(t, 7.0) for t in (q, k, v)]
+        ssa.bwd(dout, q, k, v, out, lse, cu, max(lens), decision_bitmap=bm, dq=grads[0], dk=grads[1], dv=grads[2])
+        ssa.check_device()
+        ends.append(bm)
+        return [out, lse.T] + grads
+
+    want = run(q, k, v, dout)
+    if tsf:  # the last tile (8) of the first sequence: blocks 2i and 2i + 1 share a CTA
+        last = (ends[0][:, :8, 0] >> 8) & 1
+        pairs = last.view(H, 4, 2).sum(-1)
+        assert all((pairs == m).any() for m in (0, 1, 2)), pairs
+    units = torch.tensor([u for u, seq in enumerate([0] * 9 + [1] * 2 + [2] + [3] * 5 + [4]) if seq != 2], device="cuda")
+    for bad in (math.nan, math.inf, -math.inf):
+        poisoned = [t.clone() for t in (q, k, v, dout)]
+        for t in poisoned:
+            t[n:] = bad
+        for w, g in zip(want, run(*poisoned)):
+            assert same(w.contiguous(), g.contiguous())
+        assert torch.equal(ends[0], ends[-1])
+        for t in poisoned:
+            t[lo:hi] = bad
+        for w, g in zip(want, run(*poisoned)):
+            for part in (slice(0, lo), slice(hi, n), slice(n, n + extra)):
+                assert same(w[part].contiguous(), g[part].contiguous())
+        assert torch.equal(ends[0][:, units], ends[-1][:, units])

@@ -669,8 +669,9 @@ def _rows_overlap(a, a_stride, b, b_stride):
     return d < wa or d + wb > sa
 
 
-def _check_rotary_outputs(dev, total, dim, inputs, xs, outputs, ys):
-    """Checks of rotary's given outputs; fills in their token strides."""
+def _check_rotary_outputs(dev, total, dim, inputs, xs, outputs, ys, tables):
+    """Checks of rotary's given outputs; fills in their token strides.
+    ``tables``: the contiguous (tensor, name) that the kernel reads besides."""
     written = []
     for i, (o, x, name) in enumerate(zip(outputs, inputs, ("out_q", "out_k"))):
         if o is None:
@@ -685,6 +686,10 @@ def _check_rotary_outputs(dev, total, dim, inputs, xs, outputs, ys):
             if y is None or (y is x and o.data_ptr() == x.data_ptr() and ys[i] == stride):
                 continue  # in place: a pair is read and written by one thread
             if _rows_overlap(o, ys[i], y, stride):
+                raise ValueError(f"{name} overlaps {other}")
+        start, size = o.data_ptr(), ((total - 1) * ys[i] + o.shape[1] * dim) * o.element_size() if total else 0
+        for t, other in tables:
+            if start < t.data_ptr() + t.numel() * t.element_size() and t.data_ptr() < start + size:
                 raise ValueError(f"{name} overlaps {other}")
     if len(written) == 2 and _rows_overlap(*written[0], *written[1]):
         raise ValueError("out_q overlaps out_k")
@@ -726,7 +731,8 @@ def rotary(q, k, positions, inv_freq, sections=None, interleaved: bool = False, 
     Hk = 0 if k is None else k.shape[1]
     ys = [H * D, Hk * D]
     if out_q is not None or out_k is not None:
-        _check_rotary_outputs(dev, total, D, (q, k), xs, (out_q, out_k), ys)
+        _check_rotary_outputs(dev, total, D, (q, k), xs, (out_q, out_k), ys,
+                              ((positions, "positions"), (inv_freq, "inv_freq")))
     n_pairs = _sections_type(axes)(*counts)
 
     def body(handle):

@@ -162,6 +162,31 @@ def test_overlap_of_strided_rows_matches_enumeration(ssa):
             assert got == truth, (n, h1, h2, s1, off)
 
 
+def test_rotary_outputs_over_the_tables(ssa):
+    """An output may not lie over the positions or the frequencies, which other
+    tokens still read."""
+    cpu = torch.device("cpu")
+    total, H, D = 6, 2, 8
+    q = torch.zeros(total, H, D, dtype=torch.bfloat16)
+    buf = torch.zeros(4 * q.numel(), dtype=torch.bfloat16)
+    out = buf[: q.numel()].view(q.shape)
+    wide = buf.view(total, 8, D)[:, :H]
+    pos, freq = torch.zeros(total, dtype=torch.int32), torch.zeros(4, dtype=torch.float64)
+
+    def check(o, pos=pos, freq=freq):
+        ssa._check_rotary_outputs(cpu, total, D, (q, None), [H * D, 0], (o, None), [H * D, 0],
+                                  ((pos, "positions"), (freq, "inv_freq")))
+
+    n = q.numel()
+    check(out)
+    check(wide)
+    check(out, pos=buf[n:n + 2 * total].view(torch.int32))  # right behind it
+    for o, kw in ((out, dict(pos=buf[n - 2:n - 2 + 2 * total].view(torch.int32))), (out, dict(freq=buf[8:24].view(torch.float64))),
+                  (wide, dict(pos=buf[64:64 + 2 * total].view(torch.int32))), (out, dict(pos=buf[:2 * total].view(torch.int32)))):
+        with pytest.raises(ValueError, match="overlaps"):
+            check(o, **kw)
+
+
 def test_rows_checks(ssa):
     cpu = torch.device("cpu")
     t = torch.zeros(5, 6, 8, dtype=torch.bfloat16)

@@ -6,7 +6,7 @@ import math
 import pytest
 
 from tests import training_ref as ref
-from tests.test_training_gpu import bitmap_for, make, same, ssa  # noqa: F401  (ssa: the fixture)
+from tests.test_training_gpu import BATCHES, bitmap_for, make, same, ssa  # noqa: F401  (ssa: the fixture)
 
 pytestmark = pytest.mark.gpu
 
@@ -24,6 +24,18 @@ def formula(ssa, dout, q, k, v, out, lse, cu, lens, bitmap=None):  # noqa: F811
     for g, w, b, name in zip(grads, want, (seen, *bound[1:]), ("dq", "dk", "dv")):
         ref.check(g, w, b, name)
     return grads
+
+
+@pytest.mark.parametrize("lens", BATCHES + [[2000, 1], [1300] * 3], ids=str)
+@pytest.mark.parametrize("H,Hk,D", [(2, 2, 128), (4, 2, 64), (16, 4, 128)])
+@pytest.mark.parametrize("tsf", [0.0, 200.0])
+def test_dq_over_the_seen_keys(ssa, lens, H, Hk, D, tsf):  # noqa: F811
+    """Keys with much in common (a position code three times the noise), which
+    cancels in dQ but would not in dS rounded once to bf16."""
+    q, k, v, dout, cu = make(lens, H, Hk, D, seed=46, amp=3.0)
+    bm = bitmap_for(ssa, lens, H) if tsf else None
+    out, lse = ssa.fwd_lse(q, k, v, cu, max(lens), tsf, decision_bitmap=bm)
+    formula(ssa, dout, q, k, v, out, lse, cu, lens, bm)
 
 
 @pytest.mark.parametrize("lens,H,Hk,D", SHAPES, ids=str)

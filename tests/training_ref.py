@@ -181,8 +181,10 @@ def rotate(x, positions, inv_freq, sections, interleaved, scale, transpose):
 
 
 def bound_dq(dout, q, k, v, out, lse, lens, bitmap=None, scale=0.0):
-    """dQ's bound of backward() over the keys a row sees alone: no term for any
-    other key."""
+    """dQ's bound over the keys a row sees alone: no term for any other key. dS
+    enters in two bf16 parts, hi + lo: lo = dS - hi is exact in fp32 (it has the
+    16 bits that hi has not) and at most U |dS|, so its own rounding leaves at
+    most U U |dS|; the sum has 2 n terms."""
     dout, q, k, v, out, lse = (t.double().cpu() for t in (dout, q, k, v, out, lse))
     total, H, D = q.shape
     G = H // k.shape[1]
@@ -202,7 +204,7 @@ def bound_dq(dout, q, k, v, out, lse, lens, bitmap=None, scale=0.0):
         rho = (err + 8 * E * (s.abs() + L.abs()[:, None] + 1)).where(seen, zero)
         mag = (dO.abs() @ V.abs().T + (dO.abs() * O.abs()).sum(1, keepdim=True)).where(seen, zero)
         eS = P * rho * dev.abs() + P * (1 + rho) * (D + 2) * E * mag
-        rS = eS + U * (dS.abs() + eS)  # after rounding to bf16
+        rS = eS + U * U * (dS.abs() + eS)
         dq[lo:hi, h] = c * (dS @ K)
-        bq[lo:hi, h] = c * (rS @ K.abs() + n * E * ((dS.abs() + rS) @ K.abs()))
+        bq[lo:hi, h] = c * (rS @ K.abs() + 2 * n * E * (1 + U) * ((dS.abs() + rS) @ K.abs()))
     return bq + (U + 4 * E) * (dq.abs() + bq) + 1e-37

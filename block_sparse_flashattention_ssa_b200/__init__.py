@@ -541,7 +541,8 @@ def bwd(dout, q, k, v, out, lse, cu_seqlens, max_seqlen: int, softmax_scale: flo
         dq=None, dk=None, dv=None, workspace=None, stream=None):
     """Gradients of fwd_lse(): returns (dq, dk, dv) in bf16 for the output
     gradient ``dout``. ``out``, ``lse`` and, when the forward skipped tiles,
-    ``decision_bitmap`` are what it wrote (the decisions count as constants).
+    ``decision_bitmap`` are what it wrote (the decisions count as constants); a
+    row whose lse is -inf takes no part, whatever stands in it elsewhere.
     Rows outside every sequence are left as they were in dq, dk and dv (when
     they are allocated here, undefined). ``workspace``: a device buffer of at
     least bwd_workspace_bytes() that no other call uses meanwhile."""

@@ -59,10 +59,10 @@
 //            been read.
 //
 // Bound by the board's power in long runs (75,600 tokens of 5 heads of 128, dense:
-// 47.3 ms, 774 TFLOP/s of the five products, 1238 of the eight formed here; 8192
-// x 24 x 128 2.73 ms), by the element-wise warps at D = 64 (8192 x 24: 1.90 ms),
+// 47.3 ms, 773 TFLOP/s of the five products, 1237 of the eight formed here; 8192
+// x 24 x 128 2.78 ms), by the element-wise warps at D = 64 (8192 x 24: 1.90 ms),
 // by the length of the walks and the launches in small batches (1024 x 2 x 64:
-// 13 us).
+// 13 to 17 us).
 //
 // Every wait is bounded in time; one that runs out records SSA_ERR_TIMEOUT in
 // the status word, the other roles leave at their next wait, in-flight loads

@@ -10,8 +10,9 @@
 // at position 300,000. One CTA holds a few tokens: its threads first fill a
 // table of (cos, sin) in shared memory, each angle computed once for all heads
 // of Q and K, then stream the heads. Bound by HBM: 2 bytes in and 2 out per
-// element of Q and K (75,600 x 40 + 40 x 128: 465 us adjacent, 456 us half, 6.7 and
-// 6.8 TB/s; 8192 x 24 + 24: 39 and 36 us).
+// element of Q and K (75,600 x 40 + 40 x 128 behind an L2 flush: 490 us adjacent,
+// 473 us half, 6.3 and 6.5 TB/s; 8192 x 24 + 24: 44 and 42 us, 39 and 37 back to
+// back).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 

@@ -255,9 +255,9 @@ int ssa_fwd_lse(const void* q, const void* k, const void* v, const int32_t* cu_s
  * the sums of dK and dV over every query head that shares the K/V head. The
  * skip decisions are taken as constants. P and dS are rounded to bf16 for the
  * products of dV and dK, and dS enters dQ's in two bf16 parts; products
- * accumulate in fp32, and the gradients are rounded to bf16 once. A key that a
- * row gives no probability, or whose tile it skipped, does not change the row's
- * dQ, whatever finite values the key and its v hold.
+ * accumulate in fp32, and the gradients are rounded to bf16 once. A key whose
+ * tile a row skipped does not change the row's dQ, nor does one that it gives no
+ * probability (where q_r.k_j and dout_r.v_j are within fp32's range).
  * Results do not depend on the order of execution.
  *   dout, out         device bf16 [total_tokens, num_heads, head_dim]
  *   lse               as ssa_fwd_lse wrote it; a row with an infinity takes no

@@ -184,7 +184,9 @@ def bound_dq(dout, q, k, v, out, lse, lens, bitmap=None, scale=0.0):
     """dQ's bound over the keys a row sees alone: no term for any other key. dS
     enters in two bf16 parts, hi + lo: lo = dS - hi is exact in fp32 (it has the
     16 bits that hi has not) and at most U |dS|, so its own rounding leaves at
-    most U U |dS|; the sum has 2 n terms."""
+    most U U |dS|; the sum has 2 n terms. (backward()'s own bound of dQ is wider:
+    it allows for one rounding of dS and for a term in the largest key, which an
+    earlier form of the kernel needed.)"""
     dout, q, k, v, out, lse = (t.double().cpu() for t in (dout, q, k, v, out, lse))
     total, H, D = q.shape
     G = H // k.shape[1]
